@@ -269,7 +269,7 @@ def _workspace_bytes(case, lens):
     if case["op"] == "decode":
         h = case["heads"]
         return 4 * B * h * (S + 64) + 64 * B * h * (case["d"] + 2) * 4 + (1 << 20)
-    return B * kv * (8 * case["budget"] + 16 * (-(-case["budget"] // case["page_len"])) + 64) + (1 << 20)
+    return B * kv * (16 * (case["budget"] + 128) + 64) + (1 << 20)
 
 
 def _spans(lens):
