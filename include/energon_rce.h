@@ -60,6 +60,8 @@ typedef enum {
 #define ENERGON_DEVICE_OK 0
 #define ENERGON_DEVICE_BAD_LENGTH 1 /* a length outside [0, pad_len] */
 #define ENERGON_DEVICE_TIMEOUT 2    /* a bounded wait inside a kernel ran out */
+#define ENERGON_DEVICE_BAD_PAGE 4   /* a page index outside the cache */
+#define ENERGON_DEVICE_NONFINITE 8  /* a key or value written to an 8-bit cache was not finite */
 
 /* Element types. */
 typedef enum { ENERGON_F32 = 0, ENERGON_F16 = 1, ENERGON_BF16 = 2 } energon_dtype;
@@ -369,6 +371,156 @@ ENERGON_API int energon_sched_plan(const energon_request* reqs, int n, double no
  */
 ENERGON_API int energon_sched_fifo(const energon_request* reqs, int n, int max_batch, int32_t* group_of,
                        int32_t* n_groups);
+
+/*
+ * ---------------------------------------------------------------- serving
+ * Operators that a program runs around the layers when it generates text with
+ * grouped heads: attention of packed prompts, the weight their keys received, a
+ * paged key/value cache in 8 bits, attention of one new token per sequence over it,
+ * and its reduction to the tokens that matter.  The pages describe the packed
+ * prompt pass only (QbitAI article, "Runtime"); they have no cache.
+ *
+ * Common rules.  n_heads is a multiple of n_kv_heads; query head j uses kv head
+ * j / (n_heads / n_kv_heads).  head_dim is 64 or 128.  q / k / v / o are rows of
+ * heads, [row][head][head_dim]; ld_* is the distance between rows in elements (at
+ * least heads * head_dim), so that parts of a fused Q | K | V row can be passed as they
+ * are.  Row pointers are 16-byte aligned and row distances a multiple of 16 bytes
+ * (else ENERGON_ERR_MISALIGNED).  `scale` multiplies q . k; it is finite and > 0.
+ * d_status is optional; bits are OR-ed into it.  What is wrong with one sequence does not
+ * stop the others: the kernels do no work only where they find ENERGON_DEVICE_TIMEOUT.
+ * Buffers written by a call do not overlap what it reads unless stated.
+ * All sums, softmax statistics and weights are fp32.  Two calls that use different
+ * outputs and workspaces may run at once.  Results do not depend on timing: no sum's
+ * order varies from run to run.
+ */
+
+/*
+ * Causal attention of a packed batch of prompts: for sequence b (rows cu_seqlens[b] ..
+ * cu_seqlens[b + 1] - 1), head j, position s:
+ *     o_j(s) = sum_{t <= s} softmax_t(scale q_j(s) . k(t)) v(t)
+ *   cu_seqlens  [batch + 1] int32 device, as energon_rce_offsets writes it
+ *   rows        rows allocated in q, k, v and o.  A sequence whose rows do not lie in
+ *               [0, rows] is skipped and sets ENERGON_DEVICE_BAD_LENGTH.
+ *   o           rows of no sequence are not written
+ *   lse         optional [n_heads, rows] fp32: log sum_{t <= s} exp(scale q . k)
+ * fp32: CUDA cores, fp32 products.  fp16 / bf16: tensor cores, fp32 sums; the
+ * probabilities are rounded to the 16-bit type for their product with v.  A value that is
+ * not finite at position t reaches the outputs of positions >= t only.
+ */
+ENERGON_API int energon_prompt_attention(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
+                                         int64_t ld_v, const int32_t* cu_seqlens, int batch, int rows, int n_heads,
+                                         int n_kv_heads, int head_dim, int dtype, float scale, void* o, int64_t ld_o,
+                                         float* lse, int32_t* d_status, void* stream);
+
+/*
+ * The attention weight that each key of the packed prompts receives from the last
+ * `window` queries of its sequence (length n), summed over the heads that share it:
+ *     weights[h][row of t] = sum_{j: kv head h} sum_{s >= max(t, n - window)}
+ *                            exp(scale q_j(s) . k_h(t) - lse_j(s))
+ *   lse      [n_heads, rows] fp32, from energon_prompt_attention on the same q and k
+ *   window   >= 1; any value >= the longest sequence means all queries
+ *   weights  out [n_kv_heads, rows] fp32: every row of a sequence is written, rows of no
+ *            sequence are not
+ * The rest as in energon_prompt_attention.
+ */
+ENERGON_API int energon_prompt_key_weights(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const float* lse,
+                                           const int32_t* cu_seqlens, int batch, int rows, int n_heads, int n_kv_heads,
+                                           int head_dim, int dtype, float scale, int window, float* weights,
+                                           int32_t* d_status, void* stream);
+
+/*
+ * A paged key/value cache in 8 bits: n_pages pages of page_len token slots.  A page holds,
+ * for every kv head, page_len rows of head_dim signed codes in [-127, 127] and one fp32
+ * scale each for keys and values; element = code * scale.  Device memory of the caller:
+ *   k_codes, v_codes  [n_pages, n_kv_heads, page_len, head_dim] int8, 16-byte aligned
+ *   k_scale, v_scale  [n_pages, n_kv_heads] fp32
+ *   weight            optional [n_pages, n_kv_heads, page_len] fp32: the attention weight
+ *                     each cached token received so far
+ * page_len is 16, 32, 64 or 128.  The struct itself is host memory, read during the call.
+ *
+ * A sequence's tokens 0 .. cache_lens[b] - 1 lie in the pages named by row b of a page
+ * table [batch, max_pages] int32 (device): token t in slot t % page_len of page
+ * table[b][t / page_len].  Entries behind the last used page are not read.  A length
+ * outside [0, max_pages * page_len] (or above a call's max_len) sets
+ * ENERGON_DEVICE_BAD_LENGTH and counts as an empty sequence; a page index outside
+ * [0, n_pages) sets ENERGON_DEVICE_BAD_PAGE and is never followed.
+ */
+typedef struct {
+    int8_t *k_codes, *v_codes;
+    float *k_scale, *v_scale;
+    float* weight;
+    int n_pages, n_kv_heads, page_len, head_dim;
+} energon_kv_cache;
+
+/*
+ * Writes new tokens to the cache.  Sequence b brings the rows cu_seqlens[b] ..
+ * cu_seqlens[b + 1] - 1 of k and v (none to all of its tokens); cache_lens[b] is its length
+ * WITH them, so they take the slots cache_lens[b] - n_b .. cache_lens[b] - 1.
+ *   weights   optional [n_kv_heads, rows] fp32: weights the tokens start with (from
+ *             energon_prompt_key_weights); NULL starts them at 0.  Used when the cache has
+ *             `weight`.
+ * A page whose first slot is written takes the scale max|x| * (1/127) over the new tokens
+ * it receives, per kv head (1/127 rounded to fp32).  A page that holds earlier tokens
+ * keeps its scale where that covers the new tokens; else the scale doubles until it does,
+ * and the codes of its other slots are halved as often, rounded once per call: whatever the
+ * number of tokens added one by one, an element is off by less than one final scale.  A code is the
+ * fp32 quotient element / scale rounded to the nearest integer, ties to even.  Scales below
+ * the normal fp32 range are held as 0.  NaN is stored as 0 and an infinity as +-127, neither
+ * counts for the scale, and ENERGON_DEVICE_NONFINITE is set.
+ * Otherwise slots that receive no token keep their codes.  A sequence with more new tokens
+ * than its length sets ENERGON_DEVICE_BAD_LENGTH and is skipped.  A page must belong to one sequence.
+ */
+ENERGON_API int energon_kv_append(const energon_kv_cache* cache, const int32_t* page_table, int max_pages,
+                                  const int32_t* cache_lens, const void* k, int64_t ld_k, const void* v, int64_t ld_v,
+                                  const float* weights, const int32_t* cu_seqlens, int batch, int rows, int dtype,
+                                  int32_t* d_status, void* stream);
+
+/*
+ * Attention of one new token per sequence over its cached tokens:
+ *     o_j = sum_{t < cache_lens[b]} softmax_t(scale q_j . K(t)) V(t)
+ *   q, o        [batch] rows of n_heads heads, dtype fp32, fp16 or bf16
+ *   max_len     no cache_lens entry is larger (sizes the launch and the workspace)
+ *   lse         optional [batch, n_heads] fp32: log sum_t exp(scale q . K(t))
+ *   accumulate  nonzero: adds each token's probabilities, summed over the query heads of
+ *               its kv head, to cache->weight (required then).  Sequences may share pages
+ *               (a common prefix); with accumulate the order in which they add to a shared
+ *               page is not fixed.
+ * An empty sequence gives o = 0 and lse = -infinity.  Tokens of a bad page count as masked.
+ *   workspace   energon_cache_attention_workspace_bytes bytes, 256-byte aligned; its contents
+ *               need not be kept between calls.  Calls that may overlap need their own.
+ */
+ENERGON_API size_t energon_cache_attention_workspace_bytes(const energon_kv_cache* cache, int batch, int max_len,
+                                                           int n_heads, int accumulate);
+ENERGON_API int energon_cache_attention(const energon_kv_cache* cache, const int32_t* page_table, int max_pages,
+                                        const int32_t* cache_lens, int batch, int max_len, const void* q, int64_t ld_q,
+                                        int n_heads, int dtype, float scale, void* o, int64_t ld_o, float* lse,
+                                        int accumulate, int32_t* d_status, void* workspace, size_t ws_bytes,
+                                        void* stream);
+
+/*
+ * Cuts each sequence to at most `budget` tokens: per kv head the last `recent` tokens and,
+ * of the others, those of the largest cache->weight (equal weights: the lower position; a
+ * NaN counts as the lowest weight).  The kept tokens, in their order, fill the slots 0 ..
+ * of the pages named by new_page_table [batch, new_max_pages]; weights move with them.  Each
+ * kv head keeps its own tokens, all keep the same number.
+ *   new_lens    out [batch] int32: min(cache_lens[b], budget); may be cache_lens
+ *   budget      >= 1, at most new_max_pages * page_len;  0 <= recent <= budget
+ * A new page's scale is the largest scale among the old pages its tokens come from; a code
+ * is multiplied by the fp32 quotient old scale / new scale and rounded to the nearest
+ * integer, ties to even (tokens of the page with the largest scale keep their codes).  Slots
+ * that receive no token keep theirs.
+ * A sequence of at most `budget` tokens is copied.  The new pages are other pages than the
+ * old ones, or row b of new_page_table begins with the same pages as row b of page_table:
+ * then the sequence is cut in place (nothing is done where nothing is cut).  Old pages are
+ * otherwise left as they were.  A page must belong to one sequence.
+ * Sequences with a bad length or page are left alone and get new_lens 0.
+ *   workspace   energon_cache_evict_workspace_bytes bytes, 256-byte aligned; as above
+ */
+ENERGON_API size_t energon_cache_evict_workspace_bytes(const energon_kv_cache* cache, int batch, int budget);
+ENERGON_API int energon_cache_evict(const energon_kv_cache* cache, const int32_t* page_table, int max_pages,
+                                    const int32_t* cache_lens, const int32_t* new_page_table, int new_max_pages,
+                                    int32_t* new_lens, int batch, int max_len, int budget, int recent,
+                                    int32_t* d_status, void* workspace, size_t ws_bytes, void* stream);
 
 /* Message describing the last failed call on this thread ("" if none). */
 ENERGON_API const char* energon_last_error(void);

@@ -28,6 +28,8 @@ ENERGON_ERR_DEVICE_TIMEOUT = 6
 ENERGON_DEVICE_OK = 0
 ENERGON_DEVICE_BAD_LENGTH = 1
 ENERGON_DEVICE_TIMEOUT = 2
+ENERGON_DEVICE_BAD_PAGE = 4
+ENERGON_DEVICE_NONFINITE = 8
 
 ENERGON_F32, ENERGON_F16, ENERGON_BF16 = 0, 1, 2
 TORCH_DTYPE = {ENERGON_F32: torch.float32, ENERGON_F16: torch.float16, ENERGON_BF16: torch.bfloat16}
@@ -39,7 +41,9 @@ EXPORTED = ("energon_rce_offsets", "energon_rce_remove_padding", "energon_rce_re
             "energon_trace_start", "energon_trace_stop", "energon_rce_remove_padding_noalloc",
             "energon_rce_transpose_padding_rebuild", "energon_rce_transpose_padding_remove",
             "energon_sched_plan", "energon_sched_fifo", "energon_kernel_binary_version",
-            "energon_layer_fold_weights")
+            "energon_layer_fold_weights", "energon_prompt_attention", "energon_prompt_key_weights",
+            "energon_kv_append", "energon_cache_attention_workspace_bytes", "energon_cache_attention",
+            "energon_cache_evict_workspace_bytes", "energon_cache_evict")
 ENERGON_NOALLOC_MAX_BATCH = 16384
 WEIGHT_FIELDS = ("ln1_g", "ln1_b", "w_qkv", "b_qkv", "w_o", "b_o",
                  "ln2_g", "ln2_b", "w_1", "b_1", "w_2", "b_2")
@@ -68,6 +72,11 @@ class energon_trace_entry(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 48), ("launches", ctypes.c_int), ("total_ms", ctypes.c_double)]
 
 
+class energon_kv_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "v_codes", "k_scale", "v_scale", "weight")] + \
+               [(n, ctypes.c_int) for n in ("n_pages", "n_kv_heads", "page_len", "head_dim")]
+
+
 _lib = None
 
 
@@ -79,7 +88,9 @@ def load() -> ctypes.CDLL:
             raise RuntimeError(f"{LIB_PATH} is missing: build it with `python -m padding_free_varlen_b200.build`")
         L = ctypes.CDLL(LIB_PATH)
         vp, ci, sz, u32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_uint32
+        i64, cf = ctypes.c_int64, ctypes.c_float
         cfgp, wp = ctypes.POINTER(energon_layer_config), ctypes.POINTER(energon_layer_weights)
+        cachep = ctypes.POINTER(energon_kv_cache)
         sigs = {
             "energon_rce_offsets": ([vp, ci, ci, vp, vp, vp], ci),
             "energon_rce_remove_padding": ([vp, vp, ci, ci, ci, ci, vp, vp], ci),
@@ -100,6 +111,15 @@ def load() -> ctypes.CDLL:
             "energon_sched_plan": ([ctypes.POINTER(energon_request), ci, ctypes.c_double, ci,
                                     ctypes.POINTER(ctypes.c_double), ci, ctypes.c_double, ctypes.POINTER(ctypes.c_int32),
                                     ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32)], ci),
+            "energon_prompt_attention": ([vp, i64, vp, i64, vp, i64, vp, ci, ci, ci, ci, ci, ci, cf, vp, i64, vp, vp,
+                                          vp], ci),
+            "energon_prompt_key_weights": ([vp, i64, vp, i64, vp, vp, ci, ci, ci, ci, ci, ci, cf, ci, vp, vp, vp], ci),
+            "energon_kv_append": ([cachep, vp, ci, vp, vp, i64, vp, i64, vp, vp, ci, ci, ci, vp, vp], ci),
+            "energon_cache_attention_workspace_bytes": ([cachep, ci, ci, ci, ci], sz),
+            "energon_cache_attention": ([cachep, vp, ci, vp, ci, ci, vp, i64, ci, ci, cf, vp, i64, vp, ci, vp, vp, sz,
+                                         vp], ci),
+            "energon_cache_evict_workspace_bytes": ([cachep, ci, ci], sz),
+            "energon_cache_evict": ([cachep, vp, ci, vp, vp, ci, vp, ci, ci, ci, ci, vp, vp, sz, vp], ci),
             "energon_sched_fifo": ([ctypes.POINTER(energon_request), ci, ci, ctypes.POINTER(ctypes.c_int32),
                                     ctypes.POINTER(ctypes.c_int32)], ci),
         }
@@ -262,6 +282,137 @@ def energon_kernel_binary_version() -> int:
     v = ctypes.c_int(0)
     _check(load().energon_kernel_binary_version(ctypes.byref(v)), "energon_kernel_binary_version")
     return v.value
+
+
+# ----------------------------------------------------------------------------- serving
+
+
+def _rows(x, rows: int, ld: int, width: int, dtype: int, what: str) -> int:
+    """Device pointer of `rows` rows of `width` elements, `ld` elements apart.  A tensor may be a view
+    into wider rows (its last dimensions dense, its first of stride ld); it must be of `dtype` and
+    its memory must reach to the end of the last row."""
+    if not isinstance(x, torch.Tensor):
+        return _dev(x, what)
+    if not x.is_cuda:
+        raise ValueError(f"{what}: tensor must live on a CUDA device")
+    if x.dtype is not TORCH_DTYPE.get(dtype):
+        raise ValueError(f"{what}: a {x.dtype} tensor, the call says dtype {dtype}")
+    if rows > 0 and width > 0:
+        end = (rows - 1) * ld + width
+        if x.is_contiguous():
+            have = x.numel()
+        elif x.dim() >= 2 and x[0].is_contiguous() and x.stride(0) == ld:
+            have = (x.shape[0] - 1) * ld + x[0].numel()
+        else:
+            raise ValueError(f"{what}: rows must be dense and {ld} elements apart")
+        if have < end:
+            raise ValueError(f"{what}: {have} elements, the call needs {end}")
+    return x.data_ptr()
+
+
+def _same_device(*tensors) -> None:
+    """The library launches on the current device: every tensor has to live there."""
+    here = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for x in tensors:
+        if isinstance(x, torch.Tensor) and x.is_cuda and x.device.index != here:
+            raise ValueError(f"a tensor on {x.device}, the current device is cuda:{here}")
+
+
+def _arg(x, nbytes: int, dtype, what: str) -> int:
+    """Device pointer of a dense tensor of `dtype` with at least `nbytes` bytes."""
+    if isinstance(x, torch.Tensor):
+        if x.dtype is not dtype:
+            raise ValueError(f"{what}: a {x.dtype} tensor, expected {dtype}")
+        _need(x, nbytes, what)
+    return _dev(x, what)
+
+
+def make_kv_cache(k_codes, v_codes, k_scale, v_scale, weight=None) -> energon_kv_cache:
+    """Cache struct of CUDA tensors (which must outlive its use): codes int8 [n_pages, n_kv_heads, page_len,
+    head_dim], scales fp32 [n_pages, n_kv_heads], weight fp32 [n_pages, n_kv_heads, page_len] or None."""
+    if k_codes.dim() != 4 or k_codes.shape != v_codes.shape:
+        raise ValueError("k_codes and v_codes: expected two [n_pages, n_kv_heads, page_len, head_dim] tensors")
+    n, kv, p, d = k_codes.shape
+    _same_device(k_codes, v_codes, k_scale, v_scale, weight)
+    return energon_kv_cache(_arg(k_codes, n * kv * p * d, torch.int8, "k_codes"),
+                            _arg(v_codes, n * kv * p * d, torch.int8, "v_codes"),
+                            _arg(k_scale, 4 * n * kv, torch.float32, "k_scale"),
+                            _arg(v_scale, 4 * n * kv, torch.float32, "v_scale"),
+                            _arg(weight, 4 * n * kv * p, torch.float32, "weight"), n, kv, p, d)
+
+
+def energon_prompt_attention(q, ld_q, k, ld_k, v, ld_v, cu_seqlens, batch, rows, n_heads, n_kv_heads, head_dim, dtype,
+                             scale, o, ld_o, lse=None, d_status=None, stream=None) -> None:
+    _same_device(q, k, v, cu_seqlens, o, lse, d_status)
+    wq, wk = n_heads * head_dim, n_kv_heads * head_dim
+    _check(load().energon_prompt_attention(
+        _rows(q, rows, ld_q, wq, dtype, "q"), ld_q, _rows(k, rows, ld_k, wk, dtype, "k"), ld_k,
+        _rows(v, rows, ld_v, wk, dtype, "v"), ld_v, _arg(cu_seqlens, 4 * (batch + 1), torch.int32, "cu_seqlens"), batch,
+        rows, n_heads, n_kv_heads, head_dim, dtype, scale, _rows(o, rows, ld_o, wq, dtype, "o"), ld_o,
+        _arg(lse, 4 * n_heads * rows, torch.float32, "lse"), _arg(d_status, 4, torch.int32, "d_status"),
+        _stream(stream)), "energon_prompt_attention")
+
+
+def energon_prompt_key_weights(q, ld_q, k, ld_k, lse, cu_seqlens, batch, rows, n_heads, n_kv_heads, head_dim, dtype,
+                               scale, window, weights, d_status=None, stream=None) -> None:
+    _same_device(q, k, lse, cu_seqlens, weights, d_status)
+    _check(load().energon_prompt_key_weights(
+        _rows(q, rows, ld_q, n_heads * head_dim, dtype, "q"), ld_q,
+        _rows(k, rows, ld_k, n_kv_heads * head_dim, dtype, "k"), ld_k,
+        _arg(lse, 4 * n_heads * rows, torch.float32, "lse"),
+        _arg(cu_seqlens, 4 * (batch + 1), torch.int32, "cu_seqlens"), batch, rows, n_heads, n_kv_heads, head_dim, dtype,
+        scale, min(int(window), 0x7fffffff), _arg(weights, 4 * n_kv_heads * rows, torch.float32, "weights"),
+        _arg(d_status, 4, torch.int32, "d_status"), _stream(stream)), "energon_prompt_key_weights")
+
+
+def energon_kv_append(cache, page_table, max_pages, cache_lens, k, ld_k, v, ld_v, weights, cu_seqlens, batch, rows, dtype,
+                      d_status=None, stream=None) -> None:
+    _same_device(page_table, cache_lens, k, v, weights, cu_seqlens, d_status)
+    width = cache.n_kv_heads * cache.head_dim
+    _check(load().energon_kv_append(
+        ctypes.byref(cache), _arg(page_table, 4 * batch * max_pages, torch.int32, "page_table"), max_pages,
+        _arg(cache_lens, 4 * batch, torch.int32, "cache_lens"), _rows(k, rows, ld_k, width, dtype, "k"), ld_k,
+        _rows(v, rows, ld_v, width, dtype, "v"), ld_v,
+        _arg(weights, 4 * cache.n_kv_heads * rows, torch.float32, "weights"),
+        _arg(cu_seqlens, 4 * (batch + 1), torch.int32, "cu_seqlens"), batch, rows, dtype,
+        _arg(d_status, 4, torch.int32, "d_status"), _stream(stream)), "energon_kv_append")
+
+
+def energon_cache_attention_workspace_bytes(cache, batch, max_len, n_heads, accumulate) -> int:
+    return int(load().energon_cache_attention_workspace_bytes(ctypes.byref(cache), batch, max_len, n_heads,
+                                                              int(accumulate)))
+
+
+def energon_cache_attention(cache, page_table, max_pages, cache_lens, batch, max_len, q, ld_q, n_heads, dtype, scale, o,
+                            ld_o, lse=None, accumulate=0, d_status=None, workspace=None, ws_bytes=0,
+                            stream=None) -> None:
+    _same_device(page_table, cache_lens, q, o, lse, d_status, workspace)
+    width = n_heads * cache.head_dim
+    _need(workspace, ws_bytes, "workspace")
+    _check(load().energon_cache_attention(
+        ctypes.byref(cache), _arg(page_table, 4 * batch * max_pages, torch.int32, "page_table"), max_pages,
+        _arg(cache_lens, 4 * batch, torch.int32, "cache_lens"), batch, max_len,
+        _rows(q, batch, ld_q, width, dtype, "q"), ld_q, n_heads, dtype, scale,
+        _rows(o, batch, ld_o, width, dtype, "o"), ld_o, _arg(lse, 4 * batch * n_heads, torch.float32, "lse"),
+        int(accumulate), _arg(d_status, 4, torch.int32, "d_status"), _dev(workspace, "workspace"), ws_bytes,
+        _stream(stream)), "energon_cache_attention")
+
+
+def energon_cache_evict_workspace_bytes(cache, batch, budget) -> int:
+    return int(load().energon_cache_evict_workspace_bytes(ctypes.byref(cache), batch, budget))
+
+
+def energon_cache_evict(cache, page_table, max_pages, cache_lens, new_page_table, new_max_pages, new_lens, batch, max_len,
+                        budget, recent, d_status=None, workspace=None, ws_bytes=0, stream=None) -> None:
+    _same_device(page_table, cache_lens, new_page_table, new_lens, d_status, workspace)
+    _need(workspace, ws_bytes, "workspace")
+    _check(load().energon_cache_evict(
+        ctypes.byref(cache), _arg(page_table, 4 * batch * max_pages, torch.int32, "page_table"), max_pages,
+        _arg(cache_lens, 4 * batch, torch.int32, "cache_lens"),
+        _arg(new_page_table, 4 * batch * new_max_pages, torch.int32, "new_page_table"), new_max_pages,
+        _arg(new_lens, 4 * batch, torch.int32, "new_lens"), batch, max_len, budget, recent,
+        _arg(d_status, 4, torch.int32, "d_status"), _dev(workspace, "workspace"), ws_bytes, _stream(stream)),
+        "energon_cache_evict")
 
 
 def energon_trace_start() -> None:

@@ -599,4 +599,216 @@ int energon_selftest_bounded_wait(int32_t* d_status, uint32_t timeout_us, void* 
     return ENERGON_OK;
 }
 
+// ------------------------------------------------------------------ serving
+
+}  // extern "C"
+
+namespace {
+
+// No exception crosses the ABI: host containers may throw when memory runs out.
+template <typename F>
+int guarded(const char* what, F&& f) {
+    try {
+        g_last_error.clear();
+        return f();
+    } catch (...) {
+        return ENERGON_ERR_CUDA;
+    }
+}
+
+int check_heads(const char* what, int n_heads, int n_kv, int head_dim, int dtype, float scale) {
+    if (dtype_bytes(dtype) == 0) return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: unknown dtype %d", what, dtype);
+    if (n_heads < 1 || n_kv < 1 || n_heads % n_kv != 0)
+        return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: n_heads %d is not a multiple of n_kv_heads %d", what, n_heads, n_kv);
+    if (n_heads > 32767) return fail(ENERGON_ERR_UNSUPPORTED, "%s: more than 32767 heads", what);
+    if (head_dim != 64 && head_dim != 128)
+        return fail(ENERGON_ERR_UNSUPPORTED, "%s: head_dim %d (supported: 64, 128)", what, head_dim);
+    if (!(scale > 0.0f) || scale > 3.0e38f)
+        return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: scale must be finite and > 0", what);
+    return ENERGON_OK;
+}
+
+// `rows` rows of `width` elements, `ld` apart; no rows need no memory.
+int check_rows_arg(const char* what, const char* name, const void* p, int rows, int64_t ld, int64_t width, int dtype) {
+    const int64_t e = (int64_t)dtype_bytes(dtype);
+    if (!p && rows > 0) return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: %s is NULL", what, name);
+    if (ld < width || ld > (int64_t)1 << 36)
+        return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: the rows of %s are %lld elements apart, a row has %lld", what, name,
+                    (long long)ld, (long long)width);
+    if ((uintptr_t)p % 16 != 0 || ld * e % 16 != 0)
+        return fail(ENERGON_ERR_MISALIGNED, "%s: %s and the distance of its rows must be multiples of 16 bytes", what, name);
+    return ENERGON_OK;
+}
+
+int check_packed(const char* what, const int32_t* cu, int batch, int rows) {
+    if (batch < 0 || rows < 0) return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: negative size", what);
+    if (rows > 0x7fffff00) return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: rows exceeds the int32 token index", what);
+    if (!cu) return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: cu_seqlens is NULL", what);
+    return ENERGON_OK;
+}
+
+int check_cache(const char* what, const energon_kv_cache* c, const int32_t* table, int max_pages, const int32_t* lens,
+                int batch) {
+    if (!c || !c->k_codes || !c->v_codes || !c->k_scale || !c->v_scale || (batch > 0 && (!table || !lens)))
+        return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: NULL pointer", what);
+    if (batch < 0 || max_pages < 1 || c->n_pages < 1 || c->n_kv_heads < 1)
+        return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: sizes must be positive", what);
+    if (batch > 65535 || c->n_kv_heads > 32767)
+        return fail(ENERGON_ERR_UNSUPPORTED, "%s: more than 65535 sequences or 32767 kv heads", what);
+    if (c->page_len != 16 && c->page_len != 32 && c->page_len != 64 && c->page_len != 128)
+        return fail(ENERGON_ERR_UNSUPPORTED, "%s: page_len %d (supported: 16, 32, 64, 128)", what, c->page_len);
+    if (c->head_dim != 64 && c->head_dim != 128)
+        return fail(ENERGON_ERR_UNSUPPORTED, "%s: head_dim %d (supported: 64, 128)", what, c->head_dim);
+    if (((uintptr_t)c->k_codes | (uintptr_t)c->v_codes) % 16 != 0)
+        return fail(ENERGON_ERR_MISALIGNED, "%s: the codes must be 16-byte aligned", what);
+    return ENERGON_OK;
+}
+
+CacheArgs cache_args(const energon_kv_cache& c, const int32_t* table, int max_pages, const int32_t* lens, int batch,
+                     int max_len, int32_t* status) {
+    CacheArgs a{};
+    a.k_codes = c.k_codes, a.v_codes = c.v_codes, a.k_scale = c.k_scale, a.v_scale = c.v_scale, a.weight = c.weight;
+    a.n_pages = c.n_pages, a.n_kv = c.n_kv_heads, a.page_len = c.page_len, a.head_dim = c.head_dim;
+    a.table = table, a.max_pages = max_pages, a.lens = lens, a.batch = batch, a.max_len = max_len, a.status = status;
+    return a;
+}
+
+int check_ws(const char* what, const void* ws, size_t have, size_t need) {
+    if (have < need || (need > 0 && !ws))
+        return fail(ENERGON_ERR_WORKSPACE_TOO_SMALL, "%s: workspace of %zu bytes, the call needs %zu", what, have, need);
+    if ((uintptr_t)ws % 256 != 0) return fail(ENERGON_ERR_MISALIGNED, "%s: workspace must be 256-byte aligned", what);
+    return ENERGON_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int energon_prompt_attention(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v, int64_t ld_v,
+                             const int32_t* cu_seqlens, int batch, int rows, int n_heads, int n_kv_heads, int head_dim,
+                             int dtype, float scale, void* o, int64_t ld_o, float* lse, int32_t* d_status, void* stream) {
+    return guarded("prompt attention", [&]() -> int {
+        const char* what = "prompt attention";
+        if (int r = check_heads(what, n_heads, n_kv_heads, head_dim, dtype, scale)) return r;
+        if (int r = check_packed(what, cu_seqlens, batch, rows)) return r;
+        const int64_t wq = (int64_t)n_heads * head_dim, wk = (int64_t)n_kv_heads * head_dim;
+        if (int r = check_rows_arg(what, "q", q, rows, ld_q, wq, dtype)) return r;
+        if (int r = check_rows_arg(what, "k", k, rows, ld_k, wk, dtype)) return r;
+        if (int r = check_rows_arg(what, "v", v, rows, ld_v, wk, dtype)) return r;
+        if (int r = check_rows_arg(what, "o", o, rows, ld_o, wq, dtype)) return r;
+        if (rows > 0 && (o == q || o == k || o == v)) return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: o must not be an input", what);
+        PromptArgs a{};
+        a.q = q, a.k = k, a.v = v, a.o = o, a.lse = lse;
+        a.ld_q = ld_q, a.ld_k = ld_k, a.ld_v = ld_v, a.ld_o = ld_o;
+        a.cu = cu_seqlens, a.batch = batch, a.rows = rows;
+        a.n_heads = n_heads, a.n_kv = n_kv_heads, a.head_dim = head_dim, a.dtype = dtype, a.scale = scale;
+        a.window = 0x7fffffff, a.status = d_status, a.timeout_ns = g_timeout_ns;
+        CK(launch_prompt(a, false, (cudaStream_t)stream), what);
+        return ENERGON_OK;
+    });
+}
+
+int energon_prompt_key_weights(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const float* lse,
+                               const int32_t* cu_seqlens, int batch, int rows, int n_heads, int n_kv_heads, int head_dim,
+                               int dtype, float scale, int window, float* weights, int32_t* d_status, void* stream) {
+    return guarded("key weights", [&]() -> int {
+        const char* what = "key weights";
+        if (int r = check_heads(what, n_heads, n_kv_heads, head_dim, dtype, scale)) return r;
+        if (int r = check_packed(what, cu_seqlens, batch, rows)) return r;
+        if (int r = check_rows_arg(what, "q", q, rows, ld_q, (int64_t)n_heads * head_dim, dtype)) return r;
+        if (int r = check_rows_arg(what, "k", k, rows, ld_k, (int64_t)n_kv_heads * head_dim, dtype)) return r;
+        if (rows > 0 && (!lse || !weights)) return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: NULL pointer", what);
+        if (window < 1) return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: window must be >= 1", what);
+        PromptArgs a{};
+        a.q = q, a.k = k, a.lse = const_cast<float*>(lse), a.weights = weights;
+        a.ld_q = ld_q, a.ld_k = ld_k;
+        a.cu = cu_seqlens, a.batch = batch, a.rows = rows;
+        a.n_heads = n_heads, a.n_kv = n_kv_heads, a.head_dim = head_dim, a.dtype = dtype, a.scale = scale;
+        a.window = window, a.status = d_status, a.timeout_ns = g_timeout_ns;
+        CK(launch_prompt(a, true, (cudaStream_t)stream), what);
+        return ENERGON_OK;
+    });
+}
+
+int energon_kv_append(const energon_kv_cache* cache, const int32_t* page_table, int max_pages, const int32_t* cache_lens,
+                      const void* k, int64_t ld_k, const void* v, int64_t ld_v, const float* weights,
+                      const int32_t* cu_seqlens, int batch, int rows, int dtype, int32_t* d_status, void* stream) {
+    return guarded("kv append", [&]() -> int {
+        const char* what = "kv append";
+        if (int r = check_cache(what, cache, page_table, max_pages, cache_lens, batch)) return r;
+        if (int r = check_packed(what, cu_seqlens, batch, rows)) return r;
+        if (dtype_bytes(dtype) == 0) return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: unknown dtype %d", what, dtype);
+        const int64_t width = (int64_t)cache->n_kv_heads * cache->head_dim;
+        if (int r = check_rows_arg(what, "k", k, rows, ld_k, width, dtype)) return r;
+        if (int r = check_rows_arg(what, "v", v, rows, ld_v, width, dtype)) return r;
+        AppendArgs a{};
+        a.c = cache_args(*cache, page_table, max_pages, cache_lens, batch, 0x7fffffff, d_status);
+        a.k = k, a.v = v, a.ld_k = ld_k, a.ld_v = ld_v, a.weights = weights, a.cu = cu_seqlens, a.rows = rows, a.dtype = dtype;
+        CK(launch_kv_append(a, (cudaStream_t)stream), what);
+        return ENERGON_OK;
+    });
+}
+
+size_t energon_cache_attention_workspace_bytes(const energon_kv_cache* cache, int batch, int max_len, int n_heads,
+                                               int accumulate) {
+    if (!cache || batch < 0 || max_len < 0 || n_heads < 1 || cache->n_kv_heads < 1) return 0;
+    return cache_attention_ws_bytes(batch, max_len, n_heads, cache->n_kv_heads, cache->head_dim, accumulate != 0);
+}
+
+int energon_cache_attention(const energon_kv_cache* cache, const int32_t* page_table, int max_pages,
+                            const int32_t* cache_lens, int batch, int max_len, const void* q, int64_t ld_q, int n_heads,
+                            int dtype, float scale, void* o, int64_t ld_o, float* lse, int accumulate, int32_t* d_status,
+                            void* workspace, size_t ws_bytes, void* stream) {
+    return guarded("cache attention", [&]() -> int {
+        const char* what = "cache attention";
+        if (int r = check_cache(what, cache, page_table, max_pages, cache_lens, batch)) return r;
+        if (int r = check_heads(what, n_heads, cache->n_kv_heads, cache->head_dim, dtype, scale)) return r;
+        if (max_len < 0 || max_len > 0x7fffff00) return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: bad max_len %d", what, max_len);
+        const int64_t width = (int64_t)n_heads * cache->head_dim;
+        if (int r = check_rows_arg(what, "q", q, batch, ld_q, width, dtype)) return r;
+        if (int r = check_rows_arg(what, "o", o, batch, ld_o, width, dtype)) return r;
+        if (batch > 0 && o == q) return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: o must not be q", what);
+        if (accumulate && !cache->weight)
+            return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: accumulate needs the cache's weight", what);
+        if (int r = check_ws(what, workspace, ws_bytes,
+                             energon_cache_attention_workspace_bytes(cache, batch, max_len, n_heads, accumulate)))
+            return r;
+        CacheAttnArgs a{};
+        a.c = cache_args(*cache, page_table, max_pages, cache_lens, batch, max_len, d_status);
+        a.q = q, a.o = o, a.ld_q = ld_q, a.ld_o = ld_o, a.lse = lse;
+        a.n_heads = n_heads, a.dtype = dtype, a.accumulate = accumulate != 0, a.scale = scale, a.ws = workspace;
+        CK(launch_cache_attention(a, (cudaStream_t)stream), what);
+        return ENERGON_OK;
+    });
+}
+
+size_t energon_cache_evict_workspace_bytes(const energon_kv_cache* cache, int batch, int budget) {
+    if (!cache || batch < 0 || budget < 1 || cache->n_kv_heads < 1) return 0;
+    return cache_evict_ws_bytes(batch, cache->n_kv_heads, budget);
+}
+
+int energon_cache_evict(const energon_kv_cache* cache, const int32_t* page_table, int max_pages,
+                        const int32_t* cache_lens, const int32_t* new_page_table, int new_max_pages, int32_t* new_lens,
+                        int batch, int max_len, int budget, int recent, int32_t* d_status, void* workspace,
+                        size_t ws_bytes, void* stream) {
+    return guarded("cache evict", [&]() -> int {
+        const char* what = "cache evict";
+        if (int r = check_cache(what, cache, page_table, max_pages, cache_lens, batch)) return r;
+        if (!cache->weight || (batch > 0 && (!new_page_table || !new_lens))) return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: NULL pointer", what);
+        if (max_len < 0 || max_len > 0x7fffff00) return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: bad max_len %d", what, max_len);
+        if (budget < 1 || recent < 0 || recent > budget)
+            return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: budget %d and recent %d (budget >= 1, 0 <= recent <= budget)", what,
+                        budget, recent);
+        if (new_max_pages < 1 || (int64_t)new_max_pages * cache->page_len < budget)
+            return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: %d new pages do not hold a budget of %d", what, new_max_pages, budget);
+        if (int r = check_ws(what, workspace, ws_bytes, energon_cache_evict_workspace_bytes(cache, batch, budget))) return r;
+        EvictArgs a{};
+        a.c = cache_args(*cache, page_table, max_pages, cache_lens, batch, max_len, d_status);
+        a.new_table = new_page_table, a.new_max_pages = new_max_pages, a.new_lens = new_lens;
+        a.budget = budget, a.recent = recent, a.ws = workspace;
+        CK(launch_cache_evict(a, (cudaStream_t)stream), what);
+        return ENERGON_OK;
+    });
+}
+
 }  // extern "C"

@@ -127,6 +127,67 @@ cudaError_t launch_attention_tc(int dtype, const void* qkv, const void* qk_lo, v
                                 int max_len, int H, int n_heads, int qkv_rows, int32_t* status, uint64_t timeout_ns,
                                 cudaStream_t st);
 
+// Packed prompts with grouped heads (energon_prompt_attention, energon_prompt_key_weights).
+struct PromptArgs {
+    const void *q, *k, *v;
+    void* o;
+    float* lse;              // attention: out, optional; key weights: in
+    float* weights;          // key weights: out [n_kv, rows]
+    int64_t ld_q, ld_k, ld_v, ld_o;
+    const int32_t* cu;
+    int batch, rows, n_heads, n_kv, head_dim, dtype;
+    float scale;
+    int window;
+    int32_t* status;
+    uint64_t timeout_ns;
+};
+cudaError_t launch_prompt(const PromptArgs& a, bool weights, cudaStream_t st);
+
+// The 8-bit paged cache and a page table over it.
+struct CacheArgs {
+    int8_t *k_codes, *v_codes;
+    float *k_scale, *v_scale, *weight;
+    int n_pages, n_kv, page_len, head_dim;
+    const int32_t* table;
+    int max_pages;
+    const int32_t* lens;
+    int batch, max_len;
+    int32_t* status;
+};
+struct AppendArgs {
+    CacheArgs c;
+    const void *k, *v;
+    int64_t ld_k, ld_v;
+    const float* weights;    // [n_kv, rows] or null
+    const int32_t* cu;
+    int rows, dtype;
+};
+cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t st);
+
+struct CacheAttnArgs {
+    CacheArgs c;
+    const void* q;
+    void* o;
+    int64_t ld_q, ld_o;
+    float* lse;
+    int n_heads, dtype, accumulate;
+    float scale;
+    void* ws;
+};
+size_t cache_attention_ws_bytes(int batch, int max_len, int n_heads, int n_kv, int head_dim, bool accumulate);
+cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t st);
+
+struct EvictArgs {
+    CacheArgs c;
+    const int32_t* new_table;
+    int new_max_pages;
+    int32_t* new_lens;
+    int budget, recent;
+    void* ws;
+};
+size_t cache_evict_ws_bytes(int batch, int n_kv, int budget);
+cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t st);
+
 // The binary version (major * 10 + minor) the runtime reports for the library's kernels.
 cudaError_t kernel_binary_version(int* version);
 

@@ -1,0 +1,74 @@
+// Device helpers shared by the serving operators (prompt attention, key weights, the 8-bit
+// key/value cache): work items of a packed batch, block reductions.
+#pragma once
+
+#include "common.cuh"
+
+namespace energon {
+
+// A bounded wait ran out earlier: no more work.  (The other bits concern single sequences; a
+// launch that stopped at them would compute what its blocks happened to start before.)
+__device__ __forceinline__ bool stopped(const int32_t* st) {
+    return st != nullptr && (*reinterpret_cast<const volatile int32_t*>(st) & ENERGON_DEVICE_TIMEOUT) != 0;
+}
+
+// Rows of sequence b of a packed batch; false (and n = 0) when they do not lie in [0, rows].
+__device__ __forceinline__ bool seq_rows(const int32_t* __restrict__ cu, int b, int rows, int& start, int& n) {
+    start = cu[b];
+    const int end = cu[b + 1];
+    n = end - start;
+    if (start >= 0 && end >= start && end <= rows) return true;
+    n = 0;
+    return false;
+}
+
+// Work item `item` of a batch in which sequence b has count(b) items (>= 0): the sequence and
+// the item's index inside it.  Every warp computes it for itself, 32 sequences at a time; the
+// result is the same in every thread.  False when there are fewer items.
+template <typename F>
+__device__ __forceinline__ bool find_item(int batch, int item, F count, int& b, int& j) {
+    const int lane = threadIdx.x & 31;
+    int before = 0;
+    for (int base = 0; base < batch; base += 32) {
+        const int n = base + lane < batch ? count(base + lane) : 0;
+        int x = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, item < before + x);
+        if (past) {
+            const int l = __ffs(past) - 1;
+            b = base + l;
+            j = item - before - __shfl_sync(0xffffffffu, x - n, l);
+            return true;
+        }
+        before += __shfl_sync(0xffffffffu, x, 31);
+    }
+    return false;
+}
+
+// Records ENERGON_DEVICE_BAD_LENGTH if some sequence's rows lie outside [0, rows]; called by
+// one warp of one block of a launch.
+__device__ __forceinline__ void check_rows(const int32_t* __restrict__ cu, int batch, int rows, int32_t* status) {
+    bool bad = false;
+    for (int b = threadIdx.x & 31; b < batch; b += 32) {
+        int s, n;
+        bad |= !seq_rows(cu, b, rows, s, n);
+    }
+    if (bad) status_or(status, ENERGON_DEVICE_BAD_LENGTH);
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+}  // namespace energon
