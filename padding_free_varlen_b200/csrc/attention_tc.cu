@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(128) attn_tc_kernel(const __grid_constant__ CU
 
 // ------------------------------------------------------------------ host side
 
-static PFN_cuTensorMapEncodeTiled_v12000 attn_encode_fn() {
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
@@ -376,7 +376,7 @@ bool attention_tc_supported(int dtype, int H, int n_heads, const void* qkv, cons
     if (dtype != ENERGON_F16 && dtype != ENERGON_BF16) return false;
     if (n_heads <= 0 || H % n_heads != 0 || H / n_heads != AHD) return false;
     if (((uintptr_t)qkv | (uintptr_t)qk_lo | (uintptr_t)o) % 16 != 0 || qkv_rows < 1) return false;
-    return attn_encode_fn() != nullptr;
+    return tensor_map_encoder() != nullptr;
 }
 
 // [rows, cols] 16-bit tensor, box 64 x box_rows, 128-byte swizzle.
@@ -387,7 +387,7 @@ static CUresult attn_tmap(CUtensorMap* m, int dtype, const void* ptr, int64_t co
     cuuint32_t estr[2] = {1, 1};
     const CUtensorMapDataType dt =
         dtype == ENERGON_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    return attn_encode_fn()(m, dt, 2, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    return tensor_map_encoder()(m, dt, 2, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }

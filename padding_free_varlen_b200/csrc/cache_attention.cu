@@ -2,7 +2,22 @@
 //
 //   x_t = c sum_d q_d K(t)_d,  K(t) = code * scale(page, head);  o = sum_t exp(x_t - lse) V(t)
 //
-// Simple form: one block per (sequence, query head) walks over the tokens, 128 at a time.
+// The cache's codes are read once: 2 d bytes per token and kv head, which bounds the call.  The
+// query heads of a kv head therefore pass over a token together, on the tensor cores
+// (mma m16n8k16, fp16 in, fp32 sums; at most 16 queries meet a tile, so that the wide
+// tcgen05 tiles would stand empty, and the codes have to pass the registers anyway to become
+// 16-bit numbers).  A code is exact in fp16.  A query row is scaled by a power of two to
+// below 2^15: fp16 and bf16 queries are then exact (bf16 elements below 2^-28 of the row's largest
+// lose bits below 2^-39 of it), fp32 queries are held as two fp16 terms (2^-22 of the element).
+// The scales stay outside the sums over d: one factor per (page, head) for the scores, and for the
+// values p * scale / (largest scale met so far), times 2^14, as fp16 (two terms for fp32
+// outputs).
+//
+// A warp takes 32 tokens at a time: K and V rows land in its own ring of STAGES buffers by
+// TMA (the box of a page's tokens, swizzled so that the 16-byte reads of the fragments hit
+// different banks), and it keeps its own running maximum, sum and output.  The block's warps are
+// joined in shared memory; the splits of a long sequence by a second kernel.
+#include <cudaTypedefs.h>
 #include <math.h>
 
 #include "internal.h"
@@ -11,20 +26,62 @@
 namespace energon {
 
 namespace {
-constexpr int DT = 128;  // tokens per step, threads per block
+constexpr int STEP = 32;     // tokens a warp takes at a time
+constexpr int CW = 4;        // warps per block
+constexpr int STAGES = 3;    // buffers per warp
+constexpr int BLOCK_STEP = STEP * CW;
+constexpr int MAX_SPLITS = 148;
+constexpr int SUPER = 32;    // steps whose page entries a warp holds (one per lane)
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
+constexpr float P_UP = 16384.0f;  // 2^14: keeps small probabilities in the normal range of fp16
 
-struct AttnWs {
-    float* scores;  // [batch][heads][stride], in units of log2 (accumulate only)
-    float* lse2;    // [batch][heads]
-    int stride;
+template <int HD>
+struct DCfg {
+    static constexpr int TILE = STEP * HD;  // bytes of K, and of V, per buffer
+    static constexpr int WARP = STAGES * 2 * TILE;
+    static constexpr int SMEM = CW * WARP + 1024;
 };
-__host__ __device__ inline AttnWs attn_ws(void* ws, int batch, int max_len, int n_heads) {
+
+// What a call keeps between its launches: per (sequence, head) log2 of the sum; per split a
+// maximum and sum and an unnormalised output; the scores (accumulate only).
+struct AttnWs {
+    float* lse2;    // [batch][heads]
+    float2* ml;     // [batch][heads][splits]
+    float* part;    // [batch][heads][splits][d]
+    float* scores;  // [batch][heads][stride], in units of log2
+    int stride, splits, chunk;
+    size_t bytes;
+};
+inline int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+AttnWs attn_ws(void* ws, int batch, int max_len, int n_heads, int n_kv, int head_dim, int accumulate) {
     AttnWs w;
-    w.stride = (max_len + 15) / 16 * 16;
-    w.lse2 = static_cast<float*>(ws);
-    w.scores = w.lse2 + ((size_t)batch * n_heads + 63) / 64 * 64;
+    const int64_t rows = (int64_t)batch * n_heads;
+    const int tiles = cdiv(n_heads / n_kv, 16);
+    // Enough blocks for two per SM where the lengths give them: a split is at least one step of
+    // every warp, and at most MAX_SPLITS are joined.
+    const int64_t blocks = (int64_t)batch * n_kv * tiles;
+    int64_t want = blocks > 0 ? cdiv(2 * 148, blocks) : 1;
+    // tokens per split are bounded too: with many sequences of different lengths short splits even out the SMs
+    const int64_t fine = cdiv(max_len, 2048);
+    if (want < fine) want = fine < 64 ? fine : 64;
+    if (want > MAX_SPLITS) want = MAX_SPLITS;
+    w.chunk = cdiv(cdiv(max_len > 0 ? max_len : 1, want), BLOCK_STEP) * BLOCK_STEP;
+    w.splits = cdiv(max_len > 0 ? max_len : 1, w.chunk);
+    w.stride = cdiv(max_len, 16) * 16;
+    size_t at = 0;
+    char* base = static_cast<char*>(ws);
+    auto take = [&](size_t n) {
+        char* p = base + at;
+        at += (n + 255) / 256 * 256;
+        return p;
+    };
+    w.lse2 = reinterpret_cast<float*>(take(rows * sizeof(float)));
+    const size_t parts = w.splits > 1 ? (size_t)rows * w.splits : 0;
+    w.ml = reinterpret_cast<float2*>(take(parts * sizeof(float2)));
+    w.part = reinterpret_cast<float*>(take(parts * head_dim * sizeof(float)));
+    w.scores = reinterpret_cast<float*>(take(accumulate ? (size_t)rows * w.stride * sizeof(float) : 0));
+    w.bytes = at;
     return w;
 }
 __device__ __forceinline__ int cached_len(const CacheArgs& c, int b, bool& bad) {
@@ -32,75 +89,447 @@ __device__ __forceinline__ int cached_len(const CacheArgs& c, int b, bool& bad) 
     bad = n < 0 || n > c.max_len || (int64_t)n > (int64_t)c.max_pages * c.page_len;
     return bad ? 0 : n;
 }
-}  // namespace
 
-template <typename T, int HD>
-__global__ void __launch_bounds__(DT) cache_attn_kernel(const CacheAttnArgs a) {
-    const CacheArgs& c = a.c;
-    if (stopped(c.status)) return;
-    __shared__ float q[HD], pr[DT], red[DT / 32];
-    __shared__ int64_t tile[DT];  // page * n_kv + head of each token of the step, -1: masked
-    const int tid = threadIdx.x, b = blockIdx.y, head = blockIdx.x, P = c.page_len;
-    const int kvh = head / (a.n_heads / c.n_kv);
-    bool bad;
-    const int n = cached_len(c, b, bad);
-    if (bad && head == 0 && tid == 0) status_or(c.status, ENERGON_DEVICE_BAD_LENGTH);
-    const AttnWs ws = attn_ws(a.ws, c.batch, c.max_len, a.n_heads);
-    for (int i = tid; i < HD; i += DT)
-        q[i] = to_f(static_cast<const T*>(a.q)[b * a.ld_q + (int64_t)head * HD + i]) * (a.scale * LOG2E);
-    float m = -INFINITY, l = 0.0f, acc = 0.0f;
-    for (int t0 = 0; t0 < n; t0 += DT) {
-        __syncthreads();
-        const int t = t0 + tid;
-        float x = -INFINITY;
-        tile[tid] = -1;
-        if (t < n) {
-            const int page = c.table[(int64_t)b * c.max_pages + t / P];
-            if ((unsigned)page < (unsigned)c.n_pages) {
-                tile[tid] = (int64_t)page * c.n_kv + kvh;
-                const int8_t* k = c.k_codes + (tile[tid] * P + t % P) * HD;
-                float s = 0.0f;
-                for (int i = 0; i < HD; i += 4) {
-                    const char4 e = *reinterpret_cast<const char4*>(k + i);
-                    s = fmaf(q[i], (float)e.x, s), s = fmaf(q[i + 1], (float)e.y, s);
-                    s = fmaf(q[i + 2], (float)e.z, s), s = fmaf(q[i + 3], (float)e.w, s);
-                }
-                x = s * c.k_scale[tile[tid]];
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Two biased codes (bytes LO and HI of w, each code + 128) as a pair of fp16: 0x6400 | byte is
+// 1024 + byte, less 1152.
+template <int LO, int HI>
+__device__ __forceinline__ uint32_t codes_f16(uint32_t w) {
+    const uint32_t x = __byte_perm(w, 0x64646464u, LO | 0x40 | (HI << 8) | 0x4000);
+    const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1152
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&x), bias);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pair_f16(float a, float b) { return pack2<__half>(a, b); }
+// What fp16 leaves of a pair.
+__device__ __forceinline__ uint32_t rest_f16(float a, float b, uint32_t hi) {
+    const float2 h = unpack2<__half>(hi);
+    return pack2<__half>(a - h.x, b - h.y);
+}
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+__device__ __forceinline__ void wait_for_earlier_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_grid_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Elements [0, N) of a row at p as floats.
+template <typename T, int N>
+__device__ __forceinline__ void load_row(const T* p, float (&x)[N]) {
+#pragma unroll
+    for (int i = 0; i < N * (int)sizeof(T) / 16; ++i) {
+        const uint4 w = reinterpret_cast<const uint4*>(p)[i];
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (sizeof(T) == 4) {
+                x[4 * i + j] = __uint_as_float(u[j]);
             } else {
-                status_or(c.status, ENERGON_DEVICE_BAD_PAGE);
+                const float2 f = unpack2<T>(u[j]);
+                x[8 * i + 2 * j] = f.x, x[8 * i + 2 * j + 1] = f.y;
             }
         }
-        if (a.accumulate && t < n) ws.scores[((int64_t)b * a.n_heads + head) * ws.stride + t] = x;
-        float mx = warp_max(x);
-        if ((tid & 31) == 0) red[tid >> 5] = mx;
-        __syncthreads();
-        float m_new = m;
-#pragma unroll
-        for (int w = 0; w < DT / 32; ++w) m_new = fmaxf(m_new, red[w]);
-        const float ms = m_new == -INFINITY ? 0.0f : m_new;
-        const float alpha = exp2f(m - ms);
-        pr[tid] = exp2f(x - ms);
-        __syncthreads();
-        l *= alpha, acc *= alpha;
-        for (int i = 0; i < min(DT, n - t0); ++i) {
-            l += pr[i];
-            if (tid < HD && tile[i] >= 0)
-                acc = fmaf(pr[i] * c.v_scale[tile[i]], (float)c.v_codes[(tile[i] * P + (t0 + i) % P) * HD + tid], acc);
-        }
-        m = m_new;
     }
-    if (tid < HD)
-        static_cast<T*>(a.o)[b * a.ld_o + (int64_t)head * HD + tid] = from_f<T>(l > 0.0f || isnan(l) ? acc / l : 0.0f);
-    if (tid == 0) {
-        const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
-        ws.lse2[b * a.n_heads + head] = lse2;
-        if (a.lse) a.lse[b * a.n_heads + head] = l == 0.0f ? -INFINITY : m * LN2 + logf(l);
+}
+}  // namespace
+
+struct SplitArgs {
+    AttnWs ws;
+    int q_tiles;
+    uint64_t timeout_ns;
+};
+
+// One block = one split of one sequence, for up to QT query heads of one kv head.  Fragment
+// layout of a warp's lane (g = lane / 4, c = lane % 4): in the scores g is the query and tokens
+// 2c, 2c + 1 of each 8 are the columns; the contraction over d takes the elements of lane c from
+// its own d / 4 consecutive ones, for queries and keys alike.  The output is held transposed, rows
+// d = (d / 8) g + j, columns queries 2c, 2c + 1, so that the probabilities need no exchange.
+template <typename T, int HD, int QT>
+__global__ void __launch_bounds__(CW * 32) cache_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
+                                                             const __grid_constant__ CUtensorMap tm_v,
+                                                             const CacheAttnArgs a, const SplitArgs sp) {
+    using C = DCfg<HD>;
+    constexpr int TERMS = sizeof(T) == 4 ? 2 : 1;
+    constexpr int R = QT / 8;          // query rows per lane
+    constexpr int KS = HD / 16;        // mma steps over d
+    constexpr int ND = HD / 8;         // outputs of a query per lane
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t bars[CW][STAGES];
+    __shared__ float sh_m[CW][QT], sh_l[CW][QT];
+    const CacheArgs& c = a.c;
+    if (stopped(c.status)) return;
+    let_next_grid_start();
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, cc = lane & 3;
+    const int split = blockIdx.x, b = blockIdx.z, P = c.page_len;
+    const int kvh = blockIdx.y / sp.q_tiles, qt = blockIdx.y % sp.q_tiles, group = a.n_heads / c.n_kv;
+    const int head0 = kvh * group + qt * QT, n_q = min(QT, group - qt * QT);
+    bool bad;
+    const int n = cached_len(c, b, bad);
+    if (bad && split == 0 && blockIdx.y == 0 && tid == 0) status_or(c.status, ENERGON_DEVICE_BAD_LENGTH);
+    const int t_begin = split * sp.ws.chunk, t_end = min(n, t_begin + sp.ws.chunk);
+    if (split > 0 && t_begin >= n) return;
+
+    if (lane == 0) {
+        for (int s = 0; s < STAGES; ++s) mbar_init(&bars[warp][s], 1);
+        fence_mbar_init();
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+    }
+    __syncwarp();
+
+    // this lane's part of the queries
+    uint32_t qf[TERMS][KS][R][2];
+    float qs[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        float x[HD / 4], most = 0.0f;
+        const bool have = g + 8 * r < n_q;
+        if (have) {
+            load_row<T, HD / 4>(static_cast<const T*>(a.q) + b * a.ld_q + (int64_t)(head0 + g + 8 * r) * HD + cc * (HD / 4), x);
+        } else {
+#pragma unroll
+            for (int i = 0; i < HD / 4; ++i) x[i] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < HD / 4; ++i) most = fmaxf(most, fabsf(x[i]));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        int e = 0;
+        if (isinf(most)) e = 129;
+        else if (most > 0.0f) frexpf(most, &e);
+        qs[r] = ldexpf(a.scale * LOG2E, e - 15);
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float u = ldexpf(x[4 * s + 2 * h], 15 - e), v = ldexpf(x[4 * s + 2 * h + 1], 15 - e);
+                qf[0][s][r][h] = pair_f16(u, v);
+                if constexpr (TERMS == 2) qf[1][s][r][h] = rest_f16(u, v, qf[0][s][r][h]);
+            }
+    }
+
+    float m[R], l[R], acc[R][ND / 2][4];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        m[r] = -INFINITY, l[r] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < ND / 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[r][i][e] = 0.0f;
+    }
+    float v_most = 0.0f;  // largest value scale met: the unit of acc
+    bool ok = true;
+    uint8_t* mine = ring + warp * C::WARP;
+    const int total = max(0, (t_end - t_begin + STEP - 1) / STEP);
+    const int steps = total > warp ? (total - warp + CW - 1) / CW : 0;  // of this warp
+    int used = 0;  // buffers filled so far: buffer used % STAGES, parity used / STAGES
+    for (int s0 = 0; s0 < steps; s0 += SUPER) {
+        // lane i: pages and scales of step s0 + i (two pages where they have 16 tokens)
+        const int now = min(SUPER, steps - s0);
+        int page[2] = {-1, -1};
+        float ks[2] = {0.0f, 0.0f}, vs[2] = {0.0f, 0.0f};
+        if (lane < now) {
+            const int t = t_begin + ((s0 + lane) * CW + warp) * STEP;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (t + 16 * h >= t_end) break;
+                const int p = c.table[(int64_t)b * c.max_pages + (t + 16 * h) / P];
+                if ((unsigned)p < (unsigned)c.n_pages) {
+                    page[h] = p;
+                    ks[h] = c.k_scale[(int64_t)p * c.n_kv + kvh];
+                    vs[h] = c.v_scale[(int64_t)p * c.n_kv + kvh];
+                } else {
+                    status_or(c.status, ENERGON_DEVICE_BAD_PAGE);
+                }
+            }
+        }
+        const float v_new = fmaxf(v_most, warp_max(fmaxf(vs[0], vs[1])));
+        if (v_new > v_most && v_most > 0.0f) {
+            const float by = v_most / v_new;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int i = 0; i < ND / 2; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[r][i][e] *= by;
+        }
+        v_most = v_new;
+        vs[0] = v_most > 0.0f ? vs[0] / v_most * P_UP : 0.0f;
+        vs[1] = v_most > 0.0f ? vs[1] / v_most * P_UP : 0.0f;
+
+        auto fetch = [&](int i) {
+            const int p0 = __shfl_sync(0xffffffffu, page[0], i), p1 = __shfl_sync(0xffffffffu, page[1], i);
+            const int at = (used + i) % STAGES;
+            if (lane == 0) {
+                const int t = t_begin + ((s0 + i) * CW + warp) * STEP;
+                uint64_t* bar = &bars[warp][at];
+                uint8_t* k = mine + at * 2 * C::TILE;
+                uint8_t* v = k + C::TILE;
+                if (P == 16) {
+                    const int live = (p0 >= 0) + (p1 >= 0);
+                    if (live) mbar_arrive_expect_tx(bar, live * C::TILE);
+                    else mbar_arrive(bar);
+                    if (p0 >= 0) {
+                        tma_load_3d(k, &tm_k, bar, 0, 0, p0 * c.n_kv + kvh);
+                        tma_load_3d(v, &tm_v, bar, 0, 0, p0 * c.n_kv + kvh);
+                    }
+                    if (p1 >= 0) {
+                        tma_load_3d(k + C::TILE / 2, &tm_k, bar, 0, 0, p1 * c.n_kv + kvh);
+                        tma_load_3d(v + C::TILE / 2, &tm_v, bar, 0, 0, p1 * c.n_kv + kvh);
+                    }
+                } else if (p0 >= 0) {
+                    mbar_arrive_expect_tx(bar, 2 * C::TILE);
+                    tma_load_3d(k, &tm_k, bar, 0, t % P, p0 * c.n_kv + kvh);
+                    tma_load_3d(v, &tm_v, bar, 0, t % P, p0 * c.n_kv + kvh);
+                } else {
+                    mbar_arrive(bar);
+                }
+            }
+        };
+        for (int i = 0; i < min(STAGES, now); ++i) fetch(i);
+        for (int i = 0; i < now; ++i) {
+            const int at = (used + i) % STAGES;
+            if (ok) ok = mbar_wait_bounded(&bars[warp][at], ((used + i) / STAGES) & 1, nullptr, sp.timeout_ns);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) {
+                // let the copies that are still in flight land before the block may end
+                for (int j = i; j < min(i + STAGES, now); ++j)
+                    mbar_wait_bounded(&bars[warp][(used + j) % STAGES], ((used + j) / STAGES) & 1, nullptr, sp.timeout_ns);
+                break;
+            }
+            const uint8_t* k = mine + at * 2 * C::TILE;
+            const uint8_t* v = k + C::TILE;
+            const int t0 = t_begin + ((s0 + i) * CW + warp) * STEP;
+
+            float x[2][2][4];  // [16 tokens][8 tokens][2 tokens of query g, 2 of query g + 8]
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int row = 16 * u + 8 * j + g;
+                    uint32_t w[HD / 16];
+#pragma unroll
+                    for (int h = 0; h < HD / 64; ++h) {
+                        const int ch = HD == 128 ? (2 * cc + h) ^ (row & 7) : cc ^ ((row >> 1) & 3);
+                        *reinterpret_cast<uint4*>(&w[4 * h]) = *reinterpret_cast<const uint4*>(k + row * HD + ch * 16);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[u][j][e] = 0.0f;
+#pragma unroll
+                    for (int s = 0; s < KS; ++s) {
+                        w[s] ^= 0x80808080u;
+                        const uint32_t b0 = codes_f16<0, 1>(w[s]), b1 = codes_f16<2, 3>(w[s]);
+#pragma unroll
+                        for (int y = 0; y < TERMS; ++y)
+                            mma_f16(x[u][j], qf[y][s][0][0], R == 2 ? qf[y][s][R - 1][0] : 0u, qf[y][s][0][1],
+                                    R == 2 ? qf[y][s][R - 1][1] : 0u, b0, b1);
+                    }
+                }
+
+            // scores in units of log2, masked; new maxima
+            const int p0 = __shfl_sync(0xffffffffu, page[0], i), p1 = __shfl_sync(0xffffffffu, page[1], i);
+            const float ks0 = __shfl_sync(0xffffffffu, ks[0], i), ks1 = __shfl_sync(0xffffffffu, ks[1], i);
+            const float vs0 = __shfl_sync(0xffffffffu, vs[0], i), vs1 = __shfl_sync(0xffffffffu, vs[1], i);
+            float alpha[R];
+            bool moved = false;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float mx = -INFINITY;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const bool there = (u ? p1 : p0) >= 0;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float& y = x[u][j][2 * r + e];
+                            y = there && t0 + 16 * u + 8 * j + 2 * cc + e < t_end ? y * (u ? ks1 : ks0) * qs[r] : -INFINITY;
+                            mx = fmaxf(mx, y);
+                        }
+                }
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                const float m_new = fmaxf(m[r], mx);
+                moved |= m_new > m[r];
+                alpha[r] = m[r] == -INFINITY ? 0.0f : exp2f(m[r] - m_new);
+                m[r] = m_new;
+                if (a.accumulate && g + 8 * r < n_q) {
+                    float* to = sp.ws.scores + ((int64_t)b * a.n_heads + head0 + g + 8 * r) * sp.ws.stride + t0 + 2 * cc;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            if (t0 + 16 * u + 8 * j + 2 * cc < t_end)
+                                *reinterpret_cast<float2*>(to + 16 * u + 8 * j) = make_float2(x[u][j][2 * r], x[u][j][2 * r + 1]);
+                }
+            }
+            if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    l[r] *= alpha[r];
+                    const float f0 = __shfl_sync(0xffffffffu, alpha[r], 8 * cc), f1 = __shfl_sync(0xffffffffu, alpha[r], 8 * cc + 4);
+#pragma unroll
+                    for (int y = 0; y < ND / 2; ++y)
+                        acc[r][y][0] *= f0, acc[r][y][1] *= f1, acc[r][y][2] *= f0, acc[r][y][3] *= f1;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const float vf = u ? vs1 : vs0;
+                uint32_t pf[TERMS][R][2];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float ms = m[r] == -INFINITY ? 0.0f : m[r];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float e0 = exp2f(x[u][j][2 * r] - ms), e1 = exp2f(x[u][j][2 * r + 1] - ms);
+                        l[r] += e0 + e1;
+                        pf[0][r][j] = pair_f16(e0 * vf, e1 * vf);
+                        if constexpr (TERMS == 2) pf[1][r][j] = rest_f16(e0 * vf, e1 * vf, pf[0][r][j]);
+                    }
+                }
+                uint32_t w[4][ND / 4];  // [tokens 2c, 2c + 1, 2c + 8, 2c + 9][this lane's d / 8 codes]
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const int row = 16 * u + 2 * cc + (h & 1) + 8 * (h >> 1);
+                    if constexpr (HD == 128) {
+                        *reinterpret_cast<uint4*>(&w[h][0]) =
+                            *reinterpret_cast<const uint4*>(v + row * HD + ((g ^ (row & 7)) << 4));
+                    } else {
+                        *reinterpret_cast<uint2*>(&w[h][0]) = *reinterpret_cast<const uint2*>(
+                            v + row * HD + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + 8 * (g & 1));
+                    }
+#pragma unroll
+                    for (int y = 0; y < ND / 4; ++y) w[h][y] ^= 0x80808080u;
+                }
+#pragma unroll
+                for (int y = 0; y < ND / 4; ++y)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t ab = __byte_perm(w[0][y], w[1][y], half ? 0x7362 : 0x5140);
+                        const uint32_t cd = __byte_perm(w[2][y], w[3][y], half ? 0x7362 : 0x5140);
+                        const uint32_t a0 = codes_f16<0, 1>(ab), a1 = codes_f16<2, 3>(ab);
+                        const uint32_t a2 = codes_f16<0, 1>(cd), a3 = codes_f16<2, 3>(cd);
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+#pragma unroll
+                            for (int z = 0; z < TERMS; ++z)
+                                mma_f16(acc[r][2 * y + half], a0, a1, a2, a3, pf[z][r][0], pf[z][r][1]);
+                    }
+            }
+            __syncwarp();  // every lane has read the buffer
+            if (i + STAGES < now) fetch(i + STAGES);
+        }
+        used += now;
+        if (!ok) break;
+    }
+    if (!ok && lane == 0) status_or(c.status, ENERGON_DEVICE_TIMEOUT);
+
+    // ---- the block's warps joined: o[w][query][d] in the ring, relative to the common maximum
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+        if (cc == 0) sh_m[warp][g + 8 * r] = m[r], sh_l[warp][g + 8 * r] = l[r];
+    }
+    if (!__syncthreads_and(ok)) return;
+    constexpr int LD = HD + 4;
+    float* out = reinterpret_cast<float*>(ring);
+    static_assert(CW * QT * LD * 4 <= CW * C::WARP, "the joined outputs fit in the ring");
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int q = 2 * cc + e + 8 * r;
+            float top = sh_m[0][q];
+#pragma unroll
+            for (int w = 1; w < CW; ++w) top = fmaxf(top, sh_m[w][q]);
+            const float mw = sh_m[warp][q];
+            const float f = mw == -INFINITY ? 0.0f : exp2f(mw - top) * (v_most * (1.0f / P_UP));
+            float* to = out + (warp * QT + q) * LD + ND * g;
+#pragma unroll
+            for (int y = 0; y < ND / 4; ++y)
+                *reinterpret_cast<float4*>(to + 4 * y) = make_float4(acc[r][2 * y][e] * f, acc[r][2 * y][2 + e] * f,
+                                                                     acc[r][2 * y + 1][e] * f, acc[r][2 * y + 1][2 + e] * f);
+        }
+    __syncthreads();
+    for (int i = tid; i < n_q * HD; i += CW * 32) {
+        const int q = i / HD, d = i % HD;
+        float top = sh_m[0][q], sum = 0.0f, o = 0.0f;
+#pragma unroll
+        for (int w = 1; w < CW; ++w) top = fmaxf(top, sh_m[w][q]);
+#pragma unroll
+        for (int w = 0; w < CW; ++w) {
+            const float mw = sh_m[w][q];
+            sum += mw == -INFINITY ? 0.0f : sh_l[w][q] * exp2f(mw - top);
+            o += out[(w * QT + q) * LD + d];
+        }
+        const int64_t row = (int64_t)b * a.n_heads + head0 + q;
+        if (sp.ws.splits > 1) {
+            sp.ws.part[(row * sp.ws.splits + split) * HD + d] = o;
+            if (d == 0) sp.ws.ml[row * sp.ws.splits + split] = make_float2(top, sum);
+        } else {
+            static_cast<T*>(a.o)[b * a.ld_o + (int64_t)(head0 + q) * HD + d] = from_f<T>(sum == 0.0f ? 0.0f : o / sum);
+            if (d == 0) {
+                sp.ws.lse2[row] = sum == 0.0f ? -INFINITY : top + log2f(sum);
+                if (a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : top * LN2 + logf(sum);
+            }
+        }
     }
 }
 
-// weight(t) += sum over the heads of the group of exp2(score - lse)
-__global__ void __launch_bounds__(256) cache_weight_kernel(const CacheAttnArgs a) {
+// The splits of one (sequence, query head) joined: one thread per output.
+template <typename T, int HD>
+__global__ void __launch_bounds__(HD) cache_join_kernel(const CacheAttnArgs a, const AttnWs ws) {
     const CacheArgs& c = a.c;
+    __shared__ float f[MAX_SPLITS], sum;
+    let_next_grid_start();
+    wait_for_earlier_grid();
+    if (stopped(c.status)) return;
+    const int head = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+    bool bad;
+    const int n = cached_len(c, b, bad);
+    const int live = max(1, (n + ws.chunk - 1) / ws.chunk);
+    const int64_t row = (int64_t)b * a.n_heads + head;
+    if (tid < 32) {
+        float top = -INFINITY;
+        for (int s = tid; s < live; s += 32) top = fmaxf(top, ws.ml[row * ws.splits + s].x);
+        top = warp_max(top);
+        float l = 0.0f;
+        for (int s = tid; s < live; s += 32) {
+            const float2 ml = ws.ml[row * ws.splits + s];
+            f[s] = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - top);
+            l += ml.x == -INFINITY ? 0.0f : ml.y * f[s];
+        }
+        l = warp_sum(l);
+        if (tid == 0) {
+            sum = l;
+            ws.lse2[row] = l == 0.0f ? -INFINITY : top + log2f(l);
+            if (a.lse) a.lse[row] = l == 0.0f ? -INFINITY : top * LN2 + logf(l);
+        }
+    }
+    __syncthreads();
+    const float* part = ws.part + row * ws.splits * HD + tid;
+    float o = 0.0f;
+#pragma unroll 8
+    for (int s = 0; s < live; ++s) o += part[(int64_t)s * HD] * f[s];
+    static_cast<T*>(a.o)[b * a.ld_o + (int64_t)head * HD + tid] = from_f<T>(sum == 0.0f ? 0.0f : o / sum);
+}
+
+// weight(t) += sum over the heads of the group of exp2(score - lse)
+__global__ void __launch_bounds__(256) cache_weight_kernel(const CacheAttnArgs a, const AttnWs ws) {
+    const CacheArgs& c = a.c;
+    wait_for_earlier_grid();
     if (stopped(c.status)) return;
     const int b = blockIdx.z, kvh = blockIdx.y, group = a.n_heads / c.n_kv, P = c.page_len;
     bool bad;
@@ -108,7 +537,6 @@ __global__ void __launch_bounds__(256) cache_weight_kernel(const CacheAttnArgs a
     if (t >= n) return;
     const int page = c.table[(int64_t)b * c.max_pages + t / P];
     if ((unsigned)page >= (unsigned)c.n_pages) return;
-    const AttnWs ws = attn_ws(a.ws, c.batch, c.max_len, a.n_heads);
     float sum = 0.0f;
     for (int g = 0; g < group; ++g) {
         const int64_t r = (int64_t)b * a.n_heads + kvh * group + g;
@@ -119,28 +547,70 @@ __global__ void __launch_bounds__(256) cache_weight_kernel(const CacheAttnArgs a
 }
 
 size_t cache_attention_ws_bytes(int batch, int max_len, int n_heads, int n_kv, int head_dim, bool accumulate) {
-    (void)n_kv, (void)head_dim;
-    const size_t rows = (size_t)batch * n_heads;
-    return ((rows + 63) / 64 * 64 + (accumulate ? rows * (size_t)(((int64_t)max_len + 15) / 16 * 16) : 0)) * sizeof(float);
+    return attn_ws(nullptr, batch, max_len, n_heads, n_kv, head_dim, accumulate).bytes;
+}
+
+// The codes as a [pages * heads][page_len][d] tensor of bytes, boxes of up to 32 tokens.
+static cudaError_t codes_map(CUtensorMap* m, const CacheArgs& c, const int8_t* codes) {
+    const auto encode = tensor_map_encoder();
+    if (encode == nullptr) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_len, (cuuint64_t)c.n_pages * c.n_kv};
+    const cuuint64_t strides[2] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.head_dim * c.page_len};
+    const cuuint32_t box[3] = {(cuuint32_t)c.head_dim, (cuuint32_t)(c.page_len < STEP ? c.page_len : STEP), 1};
+    const cuuint32_t one[3] = {1, 1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<int8_t*>(codes), dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, c.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
+// Launch that may start while the kernel before it ends (it waits for it itself).
+template <typename... P, typename... A>
+static cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid, cfg.blockDim = dim3(threads), cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at, cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename T, int HD, int QT>
+static cudaError_t cache_attn(const CacheAttnArgs& a, cudaStream_t st) {
+    CUtensorMap tm_k, tm_v;
+    cudaError_t e = codes_map(&tm_k, a.c, a.c.k_codes);
+    if (e == cudaSuccess) e = codes_map(&tm_v, a.c, a.c.v_codes);
+    if (e == cudaSuccess) e = prepare_smem((const void*)cache_attn_kernel<T, HD, QT>, DCfg<HD>::SMEM);
+    if (e != cudaSuccess) return e;
+    SplitArgs sp;
+    sp.ws = attn_ws(a.ws, a.c.batch, a.c.max_len, a.n_heads, a.c.n_kv, HD, a.accumulate);
+    sp.q_tiles = cdiv(a.n_heads / a.c.n_kv, QT);
+    sp.timeout_ns = a.timeout_ns;
+    const dim3 grid(sp.ws.splits, a.c.n_kv * sp.q_tiles, a.c.batch);
+    cache_attn_kernel<T, HD, QT><<<grid, CW * 32, DCfg<HD>::SMEM, st>>>(tm_k, tm_v, a, sp);
+    e = cudaGetLastError();
+    if (e == cudaSuccess && sp.ws.splits > 1)
+        e = launch_early(cache_join_kernel<T, HD>, dim3(a.n_heads, a.c.batch), HD, st, a, sp.ws);
+    if (e == cudaSuccess && a.accumulate && a.c.max_len > 0)
+        e = launch_early(cache_weight_kernel, dim3(cdiv(a.c.max_len, 256), a.c.n_kv, a.c.batch), 256, st, a, sp.ws);
+    return e;
 }
 
 template <typename T>
-static cudaError_t cache_attn(const CacheAttnArgs& a, cudaStream_t st) {
-    const dim3 grid(a.n_heads, a.c.batch);
-    if (a.c.head_dim == 64) cache_attn_kernel<T, 64><<<grid, DT, 0, st>>>(a);
-    else cache_attn_kernel<T, 128><<<grid, DT, 0, st>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || !a.accumulate || a.c.max_len == 0) return e;
-    cache_weight_kernel<<<dim3((unsigned)((a.c.max_len + 255) / 256), a.c.n_kv, a.c.batch), 256, 0, st>>>(a);
-    return cudaGetLastError();
+static cudaError_t cache_attn_t(const CacheAttnArgs& a, cudaStream_t st) {
+    const bool wide = a.n_heads / a.c.n_kv > 8;  // more than 8 queries per kv head: 16 of them meet a tile
+    if (a.c.head_dim == 64) return wide ? cache_attn<T, 64, 16>(a, st) : cache_attn<T, 64, 8>(a, st);
+    return wide ? cache_attn<T, 128, 16>(a, st) : cache_attn<T, 128, 8>(a, st);
 }
 
 cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t st) {
     if (a.c.batch <= 0) return cudaSuccess;
     switch (a.dtype) {
-    case ENERGON_F32: return cache_attn<float>(a, st);
-    case ENERGON_F16: return cache_attn<__half>(a, st);
-    case ENERGON_BF16: return cache_attn<__nv_bfloat16>(a, st);
+    case ENERGON_F32: return cache_attn_t<float>(a, st);
+    case ENERGON_F16: return cache_attn_t<__half>(a, st);
+    case ENERGON_BF16: return cache_attn_t<__nv_bfloat16>(a, st);
     }
     return cudaErrorInvalidValue;
 }

@@ -777,6 +777,7 @@ int energon_cache_attention(const energon_kv_cache* cache, const int32_t* page_t
         a.c = cache_args(*cache, page_table, max_pages, cache_lens, batch, max_len, d_status);
         a.q = q, a.o = o, a.ld_q = ld_q, a.ld_o = ld_o, a.lse = lse;
         a.n_heads = n_heads, a.dtype = dtype, a.accumulate = accumulate != 0, a.scale = scale, a.ws = workspace;
+        a.timeout_ns = g_timeout_ns;
         CK(launch_cache_attention(a, (cudaStream_t)stream), what);
         return ENERGON_OK;
     });

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -16,6 +17,8 @@ int device_cached(const void* key, int what, const std::function<int()>& compute
 // Sets a kernel's dynamic shared-memory limit on the current device once; returns the
 // cudaError_t of that one call on every later call too.
 cudaError_t prepare_smem(const void* kernel, int bytes);
+// cuTensorMapEncodeTiled of the driver, or null where it has none.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 // Offsets: cu[b+1] = cu[b] + lengths[b]; validates lengths into *status (SET).
 cudaError_t launch_offsets(const int32_t* lengths, int batch, int pad_len, int32_t* cu, int32_t* status,
@@ -173,6 +176,7 @@ struct CacheAttnArgs {
     int n_heads, dtype, accumulate;
     float scale;
     void* ws;
+    uint64_t timeout_ns;
 };
 size_t cache_attention_ws_bytes(int batch, int max_len, int n_heads, int n_kv, int head_dim, bool accumulate);
 cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t st);
