@@ -145,6 +145,7 @@ struct PromptArgs {
     uint64_t timeout_ns;
 };
 cudaError_t launch_prompt(const PromptArgs& a, bool weights, cudaStream_t st);
+cudaError_t launch_prompt_tc(const PromptArgs& a, cudaStream_t st);  // fp16, bf16
 
 // The 8-bit paged cache and a page table over it.
 struct CacheArgs {

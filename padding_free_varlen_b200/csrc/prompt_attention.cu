@@ -250,6 +250,7 @@ static cudaError_t prompt_simt(const PromptArgs& a, bool weights, cudaStream_t s
 
 cudaError_t launch_prompt(const PromptArgs& a, bool weights, cudaStream_t st) {
     if (a.batch <= 0 || a.rows <= 0) return cudaSuccess;
+    if (a.dtype != ENERGON_F32 && !weights) return launch_prompt_tc(a, st);
     switch (a.dtype) {
     case ENERGON_F32: return a.head_dim == 64 ? prompt_simt<float, 64>(a, weights, st) : prompt_simt<float, 128>(a, weights, st);
     case ENERGON_F16: return a.head_dim == 64 ? prompt_simt<__half, 64>(a, weights, st) : prompt_simt<__half, 128>(a, weights, st);
