@@ -145,7 +145,10 @@ struct PromptArgs {
     uint64_t timeout_ns;
 };
 cudaError_t launch_prompt(const PromptArgs& a, bool weights, cudaStream_t st);
-cudaError_t launch_prompt_tc(const PromptArgs& a, cudaStream_t st);  // fp16, bf16
+cudaError_t launch_prompt_tc(const PromptArgs& a, cudaStream_t st);       // fp16, bf16
+cudaError_t launch_key_weights_tc(const PromptArgs& a, cudaStream_t st);  // fp16, bf16
+// Tensor map of a [rows, cols] 16-bit tensor with rows `ld` elements apart, boxes of 64 columns, 128-byte swizzle.
+cudaError_t rows_map(CUtensorMap* m, int dtype, const void* ptr, int64_t cols, int64_t rows, int64_t ld, int box_rows);
 
 // The 8-bit paged cache and a page table over it.
 struct CacheArgs {

@@ -1,0 +1,254 @@
+// The attention weight that each key of the packed prompts receives, on the 5th-generation
+// tensor cores (fp16, bf16).
+//
+//   w_h(t) = sum_{j in group h} sum_{s >= t, s in window} exp(c q_j(s) . k_h(t) - lse_j(s))
+//
+// The products are taken transposed, X = K Q^T with 128 keys as the rows: a key is then a lane of
+// TMEM and a thread, its sum never leaves a register, and the sums lse_j(s) are one number per
+// column, read from shared memory by all lanes at once.  Per 128 x 128 tile the tensor cores need
+// 512 cycles (d = 128) and the exponentials 1024 (16 per cycle and SM), which bound the call: the
+// products of one tile run while the exponentials of the tile before are taken (two buffers in
+// TMEM), and two blocks share an SM.
+//
+// One block = 128 keys of one (sequence, kv head) and a part of the query heads that share them;
+// the blocks of a group form a cluster, whose first block adds their sums in a fixed order.
+#include <cudaTypedefs.h>
+#include <math.h>
+
+#include <type_traits>
+
+#include "internal.h"
+#include "serving.cuh"
+
+namespace energon {
+
+namespace {
+constexpr int BK = 128;            // keys per block
+constexpr int BQ = 128;            // queries per step
+constexpr int BOX = 128 * 128;     // bytes of 128 rows x 64 columns of 16 bits
+constexpr int THREADS = 128 + 96;  // a thread per key; loader, products, sums
+constexpr float LOG2E = 1.4426950408889634f;
+
+template <int HD>
+struct WCfg {
+    static constexpr int TILE = HD / 64 * BOX;
+    static constexpr int SMEM = 3 * TILE + 1024;  // keys, two buffers of queries
+};
+}  // namespace
+
+struct KeyWeightArgs {
+    PromptArgs p;
+    float c;      // scale * log2(e)
+    int cluster;  // blocks that share the heads of a group
+};
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(THREADS, 2)
+key_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const KeyWeightArgs a) {
+    using C = WCfg<HD>;
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t k_full, q_full[2], q_empty[2], l_full[2], s_full[2], s_empty[2], drain;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int dead;
+    __shared__ __align__(16) float neg_lse[2][BQ];  // -lse in units of log2
+    __shared__ float part[BK];
+    const PromptArgs& p = a.p;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // blocks of a cluster share the item; items of all kv heads pass by before the next tile of keys
+    const int64_t lin = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) / a.cluster;
+    const int rank = blockIdx.x % a.cluster, kvh = (int)(lin % p.n_kv);
+    if (lin == 0 && rank == 0 && tid < 32 && !stopped(p.status)) check_rows(p.cu, p.batch, p.rows, p.status);
+    int b, blk, start, n;
+    auto count = [&](int i) {
+        int s, len;
+        seq_rows(p.cu, i, p.rows, s, len);
+        return (len + BK - 1) / BK;
+    };
+    if (!find_item(p.batch, (int)(lin / p.n_kv), count, b, blk)) return;
+    seq_rows(p.cu, b, p.rows, start, n);
+    const int t0 = blk * BK, group = p.n_heads / p.n_kv, heads = group / a.cluster;
+    const int head0 = kvh * group + rank * heads;
+    const int begin = max(t0, n - min(p.window, n));  // first query that counts for these keys
+    const int per_head = (n - begin + BQ - 1) / BQ, steps = per_head * heads;
+
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sq = base + C::TILE;
+    if (tid == 0) {
+        mbar_init(&k_full, 1), mbar_init(&drain, 1);
+        for (int i = 0; i < 2; ++i)
+            mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 1), mbar_init(&l_full[i], 32), mbar_init(&s_full[i], 1), mbar_init(&s_empty[i], 128);
+        dead = stopped(p.status);  // the blocks of a cluster must not part: no early return
+        fence_mbar_init();
+    }
+    if (warp == 4) {
+        tmem_alloc(&tmem_slot, 2 * BQ);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const bool was_stopped = dead != 0;
+    __syncthreads();
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (mbar_wait_bounded(bar, parity, &dead, p.timeout_ns)) return true;
+        *reinterpret_cast<volatile int*>(&dead) = 1;
+        return false;
+    };
+
+    if (was_stopped) {
+        // no work
+    } else if (warp == 4) {
+        if (lane == 0) {
+            // ---- loader
+            mbar_arrive_expect_tx(&k_full, C::TILE);
+            for (int h = 0; h < HD / 64; ++h) tma_load_2d(base + h * BOX, &tm_k, &k_full, kvh * HD + 64 * h, start + t0);
+            int x = 0;
+            for (; x < steps; ++x) {
+                if (x >= 2 && !wait(&q_empty[x & 1], ((x >> 1) - 1) & 1)) break;
+                mbar_arrive_expect_tx(&q_full[x & 1], C::TILE);
+                for (int h = 0; h < HD / 64; ++h)
+                    tma_load_2d(sq + (x & 1) * C::TILE + h * BOX, &tm_q, &q_full[x & 1], (head0 + x / per_head) * HD + 64 * h,
+                                start + begin + x % per_head * BQ);
+            }
+            // all copies have landed before the block ends, also where a wait ran out
+            mbar_wait_bounded(&k_full, 0, nullptr, p.timeout_ns);
+            for (int y = max(0, x - 2); y < x; ++y) mbar_wait_bounded(&q_full[y & 1], (y >> 1) & 1, nullptr, p.timeout_ns);
+        }
+    } else if (warp == 5) {
+        if (lane == 0) {
+            // ---- products
+            constexpr uint32_t idesc = idesc_f16(std::is_same<T, __half>::value ? 0u : 1u, BK, BQ, 0);
+            bool ok = wait(&k_full, 0);
+            for (int x = 0; ok && x < steps; ++x) {
+                ok = wait(&q_full[x & 1], (x >> 1) & 1) && (x < 2 || wait(&s_empty[x & 1], ((x >> 1) - 1) & 1));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t k = smem_u32(base), q = smem_u32(sq + (x & 1) * C::TILE);
+#pragma unroll
+                for (int s = 0; s < HD / 16; ++s)
+                    umma_f16(tmem + (x & 1) * BQ, smem_desc_k128(k + (s >> 2) * BOX) + 2 * (s & 3),
+                             smem_desc_k128(q + (s >> 2) * BOX) + 2 * (s & 3), idesc, s > 0);
+                umma_commit(&s_full[x & 1]);
+                umma_commit(&q_empty[x & 1]);
+            }
+            umma_commit(&drain);  // all products are done before the block ends
+            mbar_wait_bounded(&drain, 0, nullptr, p.timeout_ns);
+        }
+    } else if (warp == 6) {
+        // ---- sums of the queries
+        for (int x = 0; x < steps; ++x) {
+            if (x >= 2 && !wait(&s_empty[x & 1], ((x >> 1) - 1) & 1)) break;
+            const float* lse = p.lse + (int64_t)(head0 + x / per_head) * p.rows + start;
+            const int s0 = begin + x % per_head * BQ;
+#pragma unroll
+            for (int i = 0; i < BQ; i += 32) {
+                const int s = s0 + i + lane;
+                neg_lse[x & 1][i + lane] = s < n ? -lse[s] * LOG2E : 0.0f;
+            }
+            mbar_arrive(&l_full[x & 1]);
+        }
+    } else {
+        // ---- exponentials, one key per thread
+        const int t = t0 + tid;
+        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        const uint64_t c2 = two(a.c, a.c);
+        uint64_t sum[2] = {two(0.0f, 0.0f), two(0.0f, 0.0f)};
+        for (int x = 0; x < steps; ++x) {
+            const int at = x & 1;
+            if (!wait(&l_full[at], (x >> 1) & 1) || !wait(&s_full[at], (x >> 1) & 1)) break;
+            tc_fence_after();
+            const int s0 = begin + x % per_head * BQ;
+            const bool edge = s0 < t0 + BK - 1 || s0 + BQ > n;
+            const int lo = t - s0, hi = n - s0;  // queries lo .. hi - 1 of the tile see this key
+#pragma unroll
+            for (int h = 0; h < BQ / 64; ++h) {
+                uint32_t r[64];
+                tmem_ld_x32(tmem + lanes + at * BQ + 64 * h, r);
+                tmem_ld_x32(tmem + lanes + at * BQ + 64 * h + 32, r + 32);
+                tmem_wait_ld_regs(r);
+                tmem_wait_ld_regs(r + 32);
+                if (64 * h >= hi) break;
+                const float4* l4 = reinterpret_cast<const float4*>(&neg_lse[at][64 * h]);
+#pragma unroll
+                for (int e = 0; e < 64; e += 4) {
+                    const float4 l = l4[e / 4];
+                    float2 u = one_by_one(fma2(two(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), c2, two(l.x, l.y)));
+                    float2 v = one_by_one(fma2(two(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])), c2, two(l.z, l.w)));
+                    if (edge) {
+                        const int i = 64 * h + e;
+                        if (i < lo || i >= hi) u.x = -INFINITY;
+                        if (i + 1 < lo || i + 1 >= hi) u.y = -INFINITY;
+                        if (i + 2 < lo || i + 2 >= hi) v.x = -INFINITY;
+                        if (i + 3 < lo || i + 3 >= hi) v.y = -INFINITY;
+                    }
+                    sum[0] = add2(sum[0], two(exp2_fast(u.x), exp2_fast(u.y)));
+                    sum[1] = add2(sum[1], two(exp2_fast(v.x), exp2_fast(v.y)));
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(&s_empty[at]);
+        }
+        const float2 u = one_by_one(add2(sum[0], sum[1]));
+        part[tid] = u.x + u.y;
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 4) tmem_dealloc(tmem, 2 * BQ);
+    if (tid == 0 && dead) status_or(p.status, ENERGON_DEVICE_TIMEOUT);
+    float w = tid < BK ? part[tid] : 0.0f;
+    bool good = dead == 0;
+    if (a.cluster > 1) {
+        cluster_sync();
+        if (rank == 0 && tid < BK) {
+            w = 0.0f;
+            for (int r = 0; r < a.cluster; ++r) {
+                float y;
+                int d;
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(y) : "r"(mapa_shared(smem_u32(&part[tid]), r)) : "memory");
+                asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(d) : "r"(mapa_shared(smem_u32(&dead), r)) : "memory");
+                w += y;
+                good = good && d == 0;
+            }
+        }
+        cluster_sync();  // no block leaves while its sums are read
+    }
+    if (rank == 0 && good && tid < BK && t0 + tid < n) p.weights[(int64_t)kvh * p.rows + start + t0 + tid] = w;
+}
+
+template <typename T, int HD>
+static cudaError_t key_weights_tc(const PromptArgs& p, cudaStream_t st) {
+    using C = WCfg<HD>;
+    CUtensorMap q, k;
+    cudaError_t e = rows_map(&q, p.dtype, p.q, (int64_t)p.n_heads * HD, p.rows, p.ld_q, BQ);
+    if (e == cudaSuccess) e = rows_map(&k, p.dtype, p.k, (int64_t)p.n_kv * HD, p.rows, p.ld_k, BK);
+    if (e == cudaSuccess) e = prepare_smem((const void*)key_weights_tc_kernel<T, HD>, C::SMEM);
+    if (e != cudaSuccess) return e;
+    KeyWeightArgs a;
+    a.p = p;
+    a.c = p.scale * LOG2E;
+    const int group = p.n_heads / p.n_kv;
+    a.cluster = 1;
+    for (int i = 2; i <= 8; ++i)
+        if (group % i == 0) a.cluster = i;
+    const int64_t most = p.rows / BK + (p.batch < p.rows ? p.batch : p.rows);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(most * a.cluster), p.n_kv), cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = C::SMEM, cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = a.cluster, at[0].val.clusterDim.y = 1, at[0].val.clusterDim.z = 1;
+    cfg.attrs = at, cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, key_weights_tc_kernel<T, HD>, q, k, a);
+}
+
+cudaError_t launch_key_weights_tc(const PromptArgs& p, cudaStream_t st) {
+    if (p.dtype == ENERGON_BF16)
+        return p.head_dim == 64 ? key_weights_tc<__nv_bfloat16, 64>(p, st) : key_weights_tc<__nv_bfloat16, 128>(p, st);
+    return p.head_dim == 64 ? key_weights_tc<__half, 64>(p, st) : key_weights_tc<__half, 128>(p, st);
+}
+
+}  // namespace energon

@@ -27,12 +27,12 @@ struct PCfg {
 
 // Rows row0 .. of a packed tensor (head offset applied) to a [64][ld] tile of floats times
 // `mul`; rows from `rows` on become 0.
-template <typename T, int HD>
-__device__ __forceinline__ void load_tile(float* dst, int ld, const T* __restrict__ src, int64_t ld_src, int rows,
+template <int HD>
+__device__ __forceinline__ void load_tile(float* dst, int ld, const float* __restrict__ src, int64_t ld_src, int rows,
                                           float mul) {
     for (int e = threadIdx.x; e < PT * HD; e += 256) {
         const int r = e / HD, d = e % HD;
-        dst[r * ld + d] = r < rows ? to_f(src[r * ld_src + d]) * mul : 0.0f;
+        dst[r * ld + d] = r < rows ? src[r * ld_src + d] * mul : 0.0f;
     }
 }
 
@@ -69,7 +69,7 @@ constexpr float LN2 = 0.6931471805599453f;
 
 // One block = 64 queries of one (sequence, head).  Scores are kept times log2(e), so that
 // the exponentials are exp2.
-template <typename T, int HD>
+template <int HD>
 __global__ void __launch_bounds__(256) prompt_simt_kernel(const PromptArgs p) {
     using C = PCfg<HD>;
     extern __shared__ float sm[];
@@ -86,10 +86,10 @@ __global__ void __launch_bounds__(256) prompt_simt_kernel(const PromptArgs p) {
     seq_rows(p.cu, b, p.rows, start, n);
     const int head = blockIdx.y, kvh = head / (p.n_heads / p.n_kv), q0 = blk * PT;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-    const T* q = static_cast<const T*>(p.q) + (int64_t)(start + q0) * p.ld_q + (int64_t)head * HD;
-    const T* k = static_cast<const T*>(p.k) + (int64_t)start * p.ld_k + (int64_t)kvh * HD;
-    const T* v = static_cast<const T*>(p.v) + (int64_t)start * p.ld_v + (int64_t)kvh * HD;
-    load_tile<T, HD>(Q, C::LD, q, p.ld_q, n - q0, p.scale * LOG2E);
+    const float* q = static_cast<const float*>(p.q) + (int64_t)(start + q0) * p.ld_q + (int64_t)head * HD;
+    const float* k = static_cast<const float*>(p.k) + (int64_t)start * p.ld_k + (int64_t)kvh * HD;
+    const float* v = static_cast<const float*>(p.v) + (int64_t)start * p.ld_v + (int64_t)kvh * HD;
+    load_tile<HD>(Q, C::LD, q, p.ld_q, n - q0, p.scale * LOG2E);
 
     float m[4], l[4], acc[4][HD / 16];
 #pragma unroll
@@ -101,8 +101,8 @@ __global__ void __launch_bounds__(256) prompt_simt_kernel(const PromptArgs p) {
     const int k_end = min(n, q0 + PT);
     for (int k0 = 0; k0 < k_end; k0 += PT) {
         __syncthreads();
-        load_tile<T, HD>(K, C::LD, k + (int64_t)k0 * p.ld_k, p.ld_k, n - k0, 1.0f);
-        load_tile<T, HD>(V, HD, v + (int64_t)k0 * p.ld_v, p.ld_v, n - k0, 1.0f);
+        load_tile<HD>(K, C::LD, k + (int64_t)k0 * p.ld_k, p.ld_k, n - k0, 1.0f);
+        load_tile<HD>(V, HD, v + (int64_t)k0 * p.ld_v, p.ld_v, n - k0, 1.0f);
         __syncthreads();
         float x[4][4];
         tile_scores<HD>(Q, K, ty, tx, x);
@@ -167,9 +167,9 @@ __global__ void __launch_bounds__(256) prompt_simt_kernel(const PromptArgs p) {
         const int s = q0 + 4 * ty + i;
         if (s >= n) continue;
         const float inv = 1.0f / l[i];
-        T* o = static_cast<T*>(p.o) + (int64_t)(start + s) * p.ld_o + (int64_t)head * HD + 4 * tx;
+        float* o = static_cast<float*>(p.o) + (int64_t)(start + s) * p.ld_o + (int64_t)head * HD + 4 * tx;
 #pragma unroll
-        for (int c = 0; c < HD / 16; ++c) o[(c >> 2) * 64 + (c & 3)] = from_f<T>(acc[i][c] * inv);
+        for (int c = 0; c < HD / 16; ++c) o[(c >> 2) * 64 + (c & 3)] = acc[i][c] * inv;
         if (p.lse != nullptr && tx == 0) p.lse[(int64_t)head * p.rows + start + s] = m[i] * LN2 + logf(l[i]);
     }
 }
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(256) prompt_simt_kernel(const PromptArgs p) {
 // One block = 64 keys of one (sequence, kv head); the queries that see them pass by in tiles
 // of 64, head after head.  Thread columns are keys: each thread sums over its rows, the 16
 // threads of a column are joined at the end in a fixed order.
-template <typename T, int HD>
+template <int HD>
 __global__ void __launch_bounds__(256) key_weights_simt_kernel(const PromptArgs p) {
     using C = PCfg<HD>;
     extern __shared__ float sm[];
@@ -196,14 +196,14 @@ __global__ void __launch_bounds__(256) key_weights_simt_kernel(const PromptArgs 
     const int kvh = blockIdx.y, group = p.n_heads / p.n_kv, t0 = blk * PT;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int first = max(t0, n - min(p.window, n));  // first query that counts for these keys
-    load_tile<T, HD>(K, C::LD, static_cast<const T*>(p.k) + (int64_t)(start + t0) * p.ld_k + (int64_t)kvh * HD, p.ld_k,
+    load_tile<HD>(K, C::LD, static_cast<const float*>(p.k) + (int64_t)(start + t0) * p.ld_k + (int64_t)kvh * HD, p.ld_k,
                      n - t0, 1.0f);
     float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int g = 0; g < group; ++g) {
         const int head = kvh * group + g;
         for (int s0 = first; s0 < n; s0 += PT) {
             __syncthreads();
-            load_tile<T, HD>(Q, C::LD, static_cast<const T*>(p.q) + (int64_t)(start + s0) * p.ld_q + (int64_t)head * HD,
+            load_tile<HD>(Q, C::LD, static_cast<const float*>(p.q) + (int64_t)(start + s0) * p.ld_q + (int64_t)head * HD,
                              p.ld_q, n - s0, p.scale * LOG2E);
             __syncthreads();
             float x[4][4];
@@ -235,29 +235,23 @@ static unsigned max_tiles(int rows, int batch, int tile) {
     return (unsigned)(rows / tile + (batch < rows ? batch : rows));
 }
 
-template <typename T, int HD>
+template <int HD>
 static cudaError_t prompt_simt(const PromptArgs& a, bool weights, cudaStream_t st) {
     using C = PCfg<HD>;
-    const void* kernel = weights ? (const void*)key_weights_simt_kernel<T, HD> : (const void*)prompt_simt_kernel<T, HD>;
+    const void* kernel = weights ? (const void*)key_weights_simt_kernel<HD> : (const void*)prompt_simt_kernel<HD>;
     const int smem = weights ? C::SMEM_W : C::SMEM;
     cudaError_t e = prepare_smem(kernel, smem);
     if (e != cudaSuccess) return e;
     const dim3 grid(max_tiles(a.rows, a.batch, PT), weights ? a.n_kv : a.n_heads);
-    if (weights) key_weights_simt_kernel<T, HD><<<grid, 256, smem, st>>>(a);
-    else prompt_simt_kernel<T, HD><<<grid, 256, smem, st>>>(a);
+    if (weights) key_weights_simt_kernel<HD><<<grid, 256, smem, st>>>(a);
+    else prompt_simt_kernel<HD><<<grid, 256, smem, st>>>(a);
     return cudaGetLastError();
 }
 
 cudaError_t launch_prompt(const PromptArgs& a, bool weights, cudaStream_t st) {
     if (a.batch <= 0 || a.rows <= 0) return cudaSuccess;
-    if (a.dtype != ENERGON_F32 && !weights) return launch_prompt_tc(a, st);
-    switch (a.dtype) {
-    case ENERGON_F32: return a.head_dim == 64 ? prompt_simt<float, 64>(a, weights, st) : prompt_simt<float, 128>(a, weights, st);
-    case ENERGON_F16: return a.head_dim == 64 ? prompt_simt<__half, 64>(a, weights, st) : prompt_simt<__half, 128>(a, weights, st);
-    case ENERGON_BF16:
-        return a.head_dim == 64 ? prompt_simt<__nv_bfloat16, 64>(a, weights, st) : prompt_simt<__nv_bfloat16, 128>(a, weights, st);
-    }
-    return cudaErrorInvalidValue;
+    if (a.dtype != ENERGON_F32) return weights ? launch_key_weights_tc(a, st) : launch_prompt_tc(a, st);
+    return a.head_dim == 64 ? prompt_simt<64>(a, weights, st) : prompt_simt<128>(a, weights, st);
 }
 
 }  // namespace energon
