@@ -36,6 +36,27 @@ struct WCfg {
 };
 }  // namespace
 
+// Adds the exponentials of 64 columns of a key's row; with EDGE only columns lo .. hi - 1 count.
+template <bool EDGE>
+__device__ __forceinline__ void add_exponentials(const uint32_t* r, const float* neg_lse, uint64_t c2, int lo, int hi,
+                                                 uint64_t (&sum)[2]) {
+    const float4* l4 = reinterpret_cast<const float4*>(neg_lse);
+#pragma unroll
+    for (int e = 0; e < 64; e += 4) {
+        const float4 l = l4[e / 4];
+        float2 u = one_by_one(fma2(two(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), c2, two(l.x, l.y)));
+        float2 v = one_by_one(fma2(two(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])), c2, two(l.z, l.w)));
+        if (EDGE) {
+            if (e < lo || e >= hi) u.x = -INFINITY;
+            if (e + 1 < lo || e + 1 >= hi) u.y = -INFINITY;
+            if (e + 2 < lo || e + 2 >= hi) v.x = -INFINITY;
+            if (e + 3 < lo || e + 3 >= hi) v.y = -INFINITY;
+        }
+        sum[0] = add2(sum[0], two(exp2_fast(u.x), exp2_fast(u.y)));
+        sum[1] = add2(sum[1], two(exp2_fast(v.x), exp2_fast(v.y)));
+    }
+}
+
 struct KeyWeightArgs {
     PromptArgs p;
     float c;      // scale * log2(e)
@@ -157,7 +178,8 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         uint64_t sum[2] = {two(0.0f, 0.0f), two(0.0f, 0.0f)};
         for (int x = 0; x < steps; ++x) {
             const int at = x & 1;
-            if (!wait(&l_full[at], (x >> 1) & 1) || !wait(&s_full[at], (x >> 1) & 1)) break;
+            const bool ok = wait(&l_full[at], (x >> 1) & 1) && wait(&s_full[at], (x >> 1) & 1);
+            if (!__all_sync(0xffffffffu, ok)) break;  // TMEM is read by whole warps
             tc_fence_after();
             const int s0 = begin + x % per_head * BQ;
             const bool edge = s0 < t0 + BK - 1 || s0 + BQ > n;
@@ -170,22 +192,8 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 tmem_wait_ld_regs(r);
                 tmem_wait_ld_regs(r + 32);
                 if (64 * h >= hi) break;
-                const float4* l4 = reinterpret_cast<const float4*>(&neg_lse[at][64 * h]);
-#pragma unroll
-                for (int e = 0; e < 64; e += 4) {
-                    const float4 l = l4[e / 4];
-                    float2 u = one_by_one(fma2(two(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), c2, two(l.x, l.y)));
-                    float2 v = one_by_one(fma2(two(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])), c2, two(l.z, l.w)));
-                    if (edge) {
-                        const int i = 64 * h + e;
-                        if (i < lo || i >= hi) u.x = -INFINITY;
-                        if (i + 1 < lo || i + 1 >= hi) u.y = -INFINITY;
-                        if (i + 2 < lo || i + 2 >= hi) v.x = -INFINITY;
-                        if (i + 3 < lo || i + 3 >= hi) v.y = -INFINITY;
-                    }
-                    sum[0] = add2(sum[0], two(exp2_fast(u.x), exp2_fast(u.y)));
-                    sum[1] = add2(sum[1], two(exp2_fast(v.x), exp2_fast(v.y)));
-                }
+                if (edge) add_exponentials<true>(r, &neg_lse[at][64 * h], c2, lo - 64 * h, hi - 64 * h, sum);
+                else add_exponentials<false>(r, &neg_lse[at][64 * h], c2, 0, 0, sum);
             }
             tc_fence_before();
             mbar_arrive(&s_empty[at]);
@@ -232,7 +240,7 @@ static cudaError_t key_weights_tc(const PromptArgs& p, cudaStream_t st) {
     a.c = p.scale * LOG2E;
     const int group = p.n_heads / p.n_kv;
     a.cluster = 1;
-    for (int i = 2; i <= 8; ++i)
+    for (int i = 2; i <= 8 && p.window > 256; ++i)
         if (group % i == 0) a.cluster = i;
     const int64_t most = p.rows / BK + (p.batch < p.rows ? p.batch : p.rows);
     cudaLaunchConfig_t cfg = {};

@@ -69,6 +69,60 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
 __device__ __forceinline__ void wg_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
 }  // namespace
 
+// Maximum of a row of N scores (this lane's) in TMEM.
+__device__ __forceinline__ float max32(const uint32_t* x) {
+    float m[4];
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+        m[y] = fmaxf(__uint_as_float(x[2 * y]), __uint_as_float(x[2 * y + 1]));
+#pragma unroll
+        for (int e = 8; e < 32; e += 8) m[y] = max3(m[y], __uint_as_float(x[e + 2 * y]), __uint_as_float(x[e + 2 * y + 1]));
+    }
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+__device__ __forceinline__ void mask32(uint32_t* x, int see) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+        if (e > see) x[e] = 0xff800000u;
+}
+template <int N, bool MASK>
+__device__ __forceinline__ float row_max(uint32_t S, int see) {
+    uint32_t x[2][32];
+    float mx = -INFINITY;
+    tmem_ld_x32(S, x[0]);
+#pragma unroll
+    for (int h = 0; h < N / 32; ++h) {
+        tmem_wait_ld_regs(x[h & 1]);
+        if (h + 1 < N / 32) tmem_ld_x32(S + 32 * (h + 1), x[(h + 1) & 1]);
+        if (MASK) mask32(x[h & 1], see - 32 * h);
+        mx = fmaxf(mx, max32(x[h & 1]));
+    }
+    return mx;
+}
+// The row's exponentials 2^(c x - mc), rounded, over its first N / 2 columns; added to `sum` unrounded.
+template <typename T, int N, bool MASK>
+__device__ __forceinline__ void exponentials(uint32_t S, float c, float mc, int see, uint64_t (&sum)[4]) {
+    const uint64_t c2 = two(c, c), m2 = two(-mc, -mc);
+    uint32_t x[2][32];
+    tmem_ld_x32(S, x[0]);
+#pragma unroll
+    for (int h = 0; h < N / 32; ++h) {
+        tmem_wait_ld_regs(x[h & 1]);
+        if (h + 1 < N / 32) tmem_ld_x32(S + 32 * (h + 1), x[(h + 1) & 1]);
+        if (MASK) mask32(x[h & 1], see - 32 * h);
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const uint32_t* y = &x[h & 1][2 * e];
+            const float2 z = one_by_one(fma2(two(__uint_as_float(y[0]), __uint_as_float(y[1])), c2, m2));
+            const float e0 = exp2_fast(z.x), e1 = exp2_fast(z.y);
+            sum[e & 3] = add2(sum[e & 3], two(e0, e1));
+            w[e] = pack2<T>(e0, e1);
+        }
+        tmem_st_x16(S + 16 * h, w);  // columns that were read before
+    }
+}
+
 struct PromptTcArgs {
     PromptArgs p;
     int pair_heads;  // NT == 2: the tiles are two heads of one kv head
@@ -135,7 +189,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (mbar_wait_bounded(bar, parity, &dead, p.timeout_ns)) return true;
+        if (wait_in_line(bar, parity, &dead, p.timeout_ns)) return true;
         *reinterpret_cast<volatile int*>(&dead) = 1;
         return false;
     };
@@ -270,26 +324,19 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t S = tmem + lanes + i * BN, O = tmem + lanes + C::O_COL + i * HD;
         float m = -INFINITY, mc = 0.0f;  // the maximum that the exponentials refer to, and times c (0 for -infinity)
-        uint64_t sum = two(0.0f, 0.0f);
+        uint64_t sum[4] = {0, 0, 0, 0};  // pairs of partial sums (+0.0)
+        // TMEM is read and written by whole warps: their lanes give up together
+        auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
         bool ok = true;
         for (int kb = 0; kb < mine; ++kb) {
-            ok = wait(&s_full[i], kb & 1);
+            ok = wait_warp(&s_full[i], kb & 1);
             if (!ok) break;
             tc_fence_after();
-            uint32_t x[BN];
-#pragma unroll
-            for (int h = 0; h < BN / 32; ++h) tmem_ld_x32(S + 32 * h, x + 32 * h);
-#pragma unroll
-            for (int h = 0; h < BN / 32; ++h) tmem_wait_ld_regs(x + 32 * h);
-            if (kb >= q0 / BN) {
-                const int see = s - kb * BN;  // keys up to here
-#pragma unroll
-                for (int e = 0; e < BN; ++e)
-                    if (e > see) x[e] = 0xff800000u;
-            }
-            float mx = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < BN; ++e) mx = fmaxf(mx, __uint_as_float(x[e]));
+            // S is read twice, 32 columns at a time with the next 32 on their way: a whole row does not
+            // fit in the registers beside the rest
+            const bool edge = kb >= q0 / BN;  // the same for the whole tile: TMEM is read by whole warps
+            const int see = s - kb * BN;      // keys up to here
+            const float mx = edge ? row_max<BN, true>(S, see) : row_max<BN, false>(S, see);
             if (kb == 0) {
                 m = mx;
                 mc = m == -INFINITY ? 0.0f : m * a.c;
@@ -300,9 +347,9 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     by = m == -INFINITY ? 0.0f : exp2_fast(mc - mx * a.c);
                     m = mx, mc = mx * a.c;
                 }
-                const float2 l = one_by_one(sum);
-                sum = two(l.x * by, l.y * by);
 #pragma unroll
+                for (int y = 0; y < 4; ++y) sum[y] = mul2(sum[y], two(by, by));
+#pragma unroll 1
                 for (int h = 0; h < HD / 32; ++h) {
                     uint32_t o[32];
                     tmem_ld_x32(O + 32 * h, o);
@@ -312,34 +359,23 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     tmem_st_x32(O + 32 * h, o);
                 }
             }
-            const uint64_t c2 = two(a.c, a.c), m2 = two(-mc, -mc);
-#pragma unroll
-            for (int h = 0; h < BN / 32; ++h) {
-                uint32_t w[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float2 y = one_by_one(fma2(two(__uint_as_float(x[32 * h + 2 * e]), __uint_as_float(x[32 * h + 2 * e + 1])), c2, m2));
-                    const float e0 = exp2_fast(y.x), e1 = exp2_fast(y.y);
-                    sum = add2(sum, two(e0, e1));
-                    w[e] = pack2<T>(e0, e1);
-                }
-                tmem_st_x16(S + 16 * h, w);
-            }
+            if (edge) exponentials<T, BN, true>(S, a.c, mc, see, sum);
+            else exponentials<T, BN, false>(S, a.c, mc, see, sum);
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&p_full[i]);
         }
-        if (mine > 0 && ok) ok = wait(&o_full[i], 0);
+        if (mine > 0 && ok) ok = wait_warp(&o_full[i], 0);
         // values that are not finite, as noted for the blocks that this tile reads
-        for (int kb = scan0; ok && kb < mine; ++kb) ok = wait(&v_ok[kb - scan0], 0);
+        for (int kb = scan0; ok && kb < mine; ++kb) ok = wait_warp(&v_ok[kb - scan0], 0);
         if (mine > 0 && ok) {
             tc_fence_after();
-            const float2 l2 = one_by_one(sum);
+            const float2 l2 = one_by_one(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
             const float l = l2.x + l2.y, inv = 1.0f / l;
             const bool fix = *reinterpret_cast<volatile int*>(&odd) != 0;
             // O / l, rounded, over the Q tile (no product reads it any more), 128-byte swizzle
             uint8_t* out = base + i * C::QT;
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < HD / 32; ++h) {
                 uint32_t o[32];
                 tmem_ld_x32(O + 32 * h, o);

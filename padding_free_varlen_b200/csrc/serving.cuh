@@ -71,6 +71,19 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
+// Bounded wait for the phase of `parity`, in line: a call would make its caller hold its registers
+// in the call's order.  Gives up like mbar_wait_bounded.
+__device__ __forceinline__ bool wait_in_line(uint64_t* bar, uint32_t parity, const volatile int* abort_flag,
+                                             uint64_t timeout_ns) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    for (uint32_t it = 1; it < (1u << 30); ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 31u) == 0 && (*abort_flag || global_ns() - t0 > timeout_ns)) return false;
+    }
+    return false;
+}
+
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ uint64_t two(float lo, float hi) {
     uint64_t r;
@@ -90,6 +103,16 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 // 2^x; results below the normal range are 0 (they would be lost in 16 bits, and in a sum >= 1).
