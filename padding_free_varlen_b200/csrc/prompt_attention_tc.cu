@@ -34,16 +34,18 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float GROW = 8.0f;            // log2 of the growth that the running maximum may lag behind
 
+constexpr int BN = 64;                  // keys per block
+
 template <int HD, int NT>
 struct TCfg {
-    static constexpr int BN = NT == 2 ? 128 : 64;            // keys per block
     static constexpr int QT = HD / 64 * QBOX;                // bytes of a Q tile
     static constexpr int KT = HD * BN * 2;                   // bytes of a K or V block
-    static constexpr int RING = NT == 2 ? (HD == 128 ? 5 : 8) : 4;
-    static constexpr int SMEM = NT * QT + RING * KT + 1024;
+    static constexpr int RING = NT == 2 ? (HD == 128 ? 5 : 8) : 2;  // buffers of K, and of V
+    static constexpr int SMEM = NT * QT + 2 * RING * KT + 1024;
     static constexpr int THREADS = NT * 128 + 128;
-    static constexpr int TMEM = NT == 2 ? 512 : (HD == 128 ? 256 : 128);
-    static constexpr int O_COL = NT * BN;
+    static constexpr int SCAN = NT == 2 ? 32 : 64;           // threads that scan V
+    static constexpr int O_COL = NT * 2 * BN;                // S takes two buffers per tile
+    static constexpr int TMEM = NT == 2 ? 512 : 256;
     static constexpr int CTAS = NT == 2 ? 1 : 2;
     static constexpr int SCANS = NT * BM / BN;               // most blocks that cross a diagonal
 };
@@ -69,58 +71,17 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
 __device__ __forceinline__ void wg_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
 }  // namespace
 
-// Maximum of a row of N scores (this lane's) in TMEM.
-__device__ __forceinline__ float max32(const uint32_t* x) {
+// Maximum of N scores.
+template <int N>
+__device__ __forceinline__ float max_of(const uint32_t* x) {
     float m[4];
 #pragma unroll
     for (int y = 0; y < 4; ++y) {
         m[y] = fmaxf(__uint_as_float(x[2 * y]), __uint_as_float(x[2 * y + 1]));
 #pragma unroll
-        for (int e = 8; e < 32; e += 8) m[y] = max3(m[y], __uint_as_float(x[e + 2 * y]), __uint_as_float(x[e + 2 * y + 1]));
+        for (int e = 8; e < N; e += 8) m[y] = max3(m[y], __uint_as_float(x[e + 2 * y]), __uint_as_float(x[e + 2 * y + 1]));
     }
     return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-}
-__device__ __forceinline__ void mask32(uint32_t* x, int see) {
-#pragma unroll
-    for (int e = 0; e < 32; ++e)
-        if (e > see) x[e] = 0xff800000u;
-}
-template <int N, bool MASK>
-__device__ __forceinline__ float row_max(uint32_t S, int see) {
-    uint32_t x[2][32];
-    float mx = -INFINITY;
-    tmem_ld_x32(S, x[0]);
-#pragma unroll
-    for (int h = 0; h < N / 32; ++h) {
-        tmem_wait_ld_regs(x[h & 1]);
-        if (h + 1 < N / 32) tmem_ld_x32(S + 32 * (h + 1), x[(h + 1) & 1]);
-        if (MASK) mask32(x[h & 1], see - 32 * h);
-        mx = fmaxf(mx, max32(x[h & 1]));
-    }
-    return mx;
-}
-// The row's exponentials 2^(c x - mc), rounded, over its first N / 2 columns; added to `sum` unrounded.
-template <typename T, int N, bool MASK>
-__device__ __forceinline__ void exponentials(uint32_t S, float c, float mc, int see, uint64_t (&sum)[4]) {
-    const uint64_t c2 = two(c, c), m2 = two(-mc, -mc);
-    uint32_t x[2][32];
-    tmem_ld_x32(S, x[0]);
-#pragma unroll
-    for (int h = 0; h < N / 32; ++h) {
-        tmem_wait_ld_regs(x[h & 1]);
-        if (h + 1 < N / 32) tmem_ld_x32(S + 32 * (h + 1), x[(h + 1) & 1]);
-        if (MASK) mask32(x[h & 1], see - 32 * h);
-        uint32_t w[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const uint32_t* y = &x[h & 1][2 * e];
-            const float2 z = one_by_one(fma2(two(__uint_as_float(y[0]), __uint_as_float(y[1])), c2, m2));
-            const float e0 = exp2_fast(z.x), e1 = exp2_fast(z.y);
-            sum[e & 3] = add2(sum[e & 3], two(e0, e1));
-            w[e] = pack2<T>(e0, e1);
-        }
-        tmem_st_x16(S + 16 * h, w);  // columns that were read before
-    }
 }
 
 struct PromptTcArgs {
@@ -136,16 +97,16 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
                  const PromptTcArgs a) {
     using C = TCfg<HD, NT>;
-    constexpr int BN = C::BN;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t q_full[NT], full[C::RING], empty[C::RING], s_full[NT], p_full[NT], o_full[NT], drain;
+    __shared__ uint64_t q_full[NT], s_full[NT][2], p_full[NT][2], o_done[NT], o_full[NT], drain[NT];
+    __shared__ uint64_t k_full[C::RING], k_empty[C::RING], v_full[C::RING], v_empty[C::RING];
     __shared__ uint64_t v_in[C::SCANS], v_ok[C::SCANS];  // blocks that are scanned: landed, scanned (used once each)
     __shared__ uint32_t tmem_slot;
     __shared__ int dead, odd;
     __shared__ int first[3][HD];  // first key whose value in this column is +inf, -inf, NaN
     const PromptArgs& p = a.p;
     if (stopped(p.status)) return;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int64_t item = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;  // heads pass by first
     if (item == 0 && tid < 32) check_rows(p.cu, p.batch, p.rows, p.status);
 
@@ -170,13 +131,17 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const int scan0 = q0_of(0) / BN;  // first block with keys behind a query
 
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* ring = base + NT * C::QT;
+    uint8_t* ring_k = base + NT * C::QT;
+    uint8_t* ring_v = ring_k + C::RING * C::KT;
     for (int i = tid; i < 3 * HD; i += C::THREADS) (&first[0][0])[i] = 0x7fffffff;
     if (tid == 0) {
-        for (int i = 0; i < NT; ++i) mbar_init(&q_full[i], 1), mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 128), mbar_init(&o_full[i], 1);
-        for (int i = 0; i < C::RING; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
-        for (int i = 0; i < C::SCANS; ++i) mbar_init(&v_in[i], 1), mbar_init(&v_ok[i], 64);
-        mbar_init(&drain, 1);
+        for (int i = 0; i < NT; ++i) {
+            mbar_init(&q_full[i], 1), mbar_init(&o_done[i], 1), mbar_init(&o_full[i], 1), mbar_init(&drain[i], 1);
+            for (int y = 0; y < 2; ++y) mbar_init(&s_full[i][y], 1), mbar_init(&p_full[i][y], 128);
+        }
+        for (int i = 0; i < C::RING; ++i)
+            mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], NT), mbar_init(&v_full[i], 1), mbar_init(&v_empty[i], NT);
+        for (int i = 0; i < C::SCANS; ++i) mbar_init(&v_in[i], 1), mbar_init(&v_ok[i], C::SCAN);
         dead = 0, odd = 0;
         fence_mbar_init();
     }
@@ -187,7 +152,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (wait_in_line(bar, parity, &dead, p.timeout_ns)) return true;
         *reinterpret_cast<volatile int*>(&dead) = 1;
@@ -196,99 +161,93 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 
     if (warp == NT * 4) {
         if (lane == 0) {
-            // ---- loader.  Buffer 2 kb of the ring's sequence is K block kb, 2 kb + 1 is V block kb.
+            // ---- loader: Q, then K(0), K(1), V(0), K(2), V(1), ...
             for (int i = 0; i < NT; ++i) {
                 if (i > 0 && nb1 == 0) break;
                 mbar_arrive_expect_tx(&q_full[i], C::QT);
                 for (int h = 0; h < HD / 64; ++h)
                     tma_load_2d(base + i * C::QT + h * QBOX, &tm_q, &q_full[i], head_of(i) * HD + 64 * h, start + q0_of(i));
             }
-            int x = 0;
-            for (; x < 2 * nb; ++x) {
-                const int at = x % C::RING;
-                if (x >= C::RING && !wait(&empty[at], (x / C::RING - 1) & 1)) break;
-                uint64_t* bar = &full[at];
-                if ((x & 1) && (x >> 1) >= scan0) {  // the scan waits for this one alone
+            int nk = 0, nv = 0;  // blocks asked for
+            for (int x = 0; x < 2 * nb; ++x) {
+                const bool keys = nk < nb && nk - nv < 2;
+                const int kb = keys ? nk : nv, at = kb % C::RING;
+                if (kb >= C::RING && !wait(keys ? &k_empty[at] : &v_empty[at], (kb / C::RING - 1) & 1)) break;
+                uint64_t* bar = keys ? &k_full[at] : &v_full[at];
+                if (!keys && kb >= scan0) {  // the scan waits for this one alone
                     mbar_arrive(bar);
-                    bar = &v_in[(x >> 1) - scan0];
+                    bar = &v_in[kb - scan0];
                 }
                 mbar_arrive_expect_tx(bar, C::KT);
                 for (int h = 0; h < HD / 64; ++h)
-                    tma_load_2d(ring + at * C::KT + h * BN * 128, x & 1 ? &tm_v : &tm_k, bar, kvh * HD + 64 * h,
-                                start + (x >> 1) * BN);
+                    tma_load_2d((keys ? ring_k : ring_v) + at * C::KT + h * BN * 128, keys ? &tm_k : &tm_v, bar,
+                                kvh * HD + 64 * h, start + kb * BN);
+                (keys ? nk : nv) += 1;
             }
             // All copies have landed before the block ends, also where a wait ran out.
             for (int i = 0; i < NT; ++i)
                 if (i == 0 || nb1 > 0) mbar_wait_bounded(&q_full[i], 0, nullptr, p.timeout_ns);
-            for (int y = max(0, x - C::RING); y < x; ++y)
-                mbar_wait_bounded(&full[y % C::RING], (y / C::RING) & 1, nullptr, p.timeout_ns);
-            for (int kb = scan0; 2 * kb + 1 < x; ++kb) mbar_wait_bounded(&v_in[kb - scan0], 0, nullptr, p.timeout_ns);
+            for (int y = max(0, nk - C::RING); y < nk; ++y)
+                mbar_wait_bounded(&k_full[y % C::RING], (y / C::RING) & 1, nullptr, p.timeout_ns);
+            for (int y = max(0, nv - C::RING); y < nv; ++y)
+                mbar_wait_bounded(&v_full[y % C::RING], (y / C::RING) & 1, nullptr, p.timeout_ns);
+            for (int kb = scan0; kb < nv; ++kb) mbar_wait_bounded(&v_in[kb - scan0], 0, nullptr, p.timeout_ns);
         }
-    } else if (warp == NT * 4 + 1) {
-        if (lane == 0) {
-            // ---- products
-            constexpr uint32_t fmt = std::is_same<T, __half>::value ? 0u : 1u;
-            constexpr uint32_t idesc_s = idesc_f16(fmt, BM, BN, 0), idesc_o = idesc_f16(fmt, BM, HD, 1);
-            auto scores = [&](int i, int kb) {
-                const uint32_t q = smem_u32(base + i * C::QT), k = smem_u32(ring + (2 * kb) % C::RING * C::KT);
+    } else if (warp > NT * 4 && warp <= NT * 4 + NT) {
+        // ---- products of tile i: the whole warp follows, one lane issues.  A warp per tile: one's
+        // products fill the time in which the other looks at its barriers.
+        constexpr uint32_t fmt = std::is_same<T, __half>::value ? 0u : 1u;
+        constexpr uint32_t idesc_s = idesc_f16(fmt, BM, BN, 0), idesc_o = idesc_f16(fmt, BM, HD, 1);
+        const int i = warp - NT * 4 - 1, mine = i == 0 ? nb0 : nb1;
+        auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+        auto have_k = [&](int kb) { return wait_warp(&k_full[kb % C::RING], (kb / C::RING) & 1); };
+        auto scores = [&](int kb) {  // and K's buffer is free once they are done
+            if (kb < mine) {
+                const uint32_t q = smem_u32(base + i * C::QT), k = smem_u32(ring_k + kb % C::RING * C::KT);
 #pragma unroll
                 for (int s = 0; s < HD / 16; ++s)
-                    umma_f16(tmem + i * BN, smem_desc_k128(q + (s >> 2) * QBOX) + 2 * (s & 3),
+                    umma_f16(tmem + (2 * i + (kb & 1)) * BN, smem_desc_k128(q + (s >> 2) * QBOX) + 2 * (s & 3),
                              smem_desc_k128(k + (s >> 2) * BN * 128) + 2 * (s & 3), idesc_s, s > 0);
-            };
-            auto have = [&](int x) { return wait(&full[x % C::RING], (x / C::RING) & 1); };
-            bool ok = wait(&q_full[0], 0) && have(0);
-            if (ok) {
-                tc_fence_after();
-                scores(0, 0);
-                umma_commit(&s_full[0]);
+                umma_commit(&s_full[i][kb & 1]);
             }
-            if (ok && NT == 2 && nb1 > 0) {
-                ok = wait(&q_full[NT - 1], 0);
-                if (ok) {
-                    scores(NT - 1, 0);
-                    umma_commit(&s_full[NT - 1]);
-                }
-            }
-            if (ok) umma_commit(&empty[0]);
-            for (int kb = 0; ok && kb < nb; ++kb) {
-                bool next = false;  // some tile reads K block kb + 1
-                for (int i = 0; ok && i < NT; ++i) {
-                    const int mine = i == 0 ? nb0 : nb1;
-                    if (kb >= mine) continue;
-                    ok = wait(&p_full[i], kb & 1) && have(2 * kb + 1) &&
-                         (kb < scan0 || (wait(&v_in[kb - scan0], 0) && wait(&v_ok[kb - scan0], 0)));
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t v = smem_u32(ring + (2 * kb + 1) % C::RING * C::KT);
+            umma_commit(&k_empty[kb % C::RING]);
+        };
+        // the scores run two blocks ahead of the products with V
+        bool ok = mine == 0 || wait_warp(&q_full[i], 0);
+        for (int kb = 0; ok && kb < 2 && kb < nb; ++kb) {
+            ok = have_k(kb);
+            tc_fence_after();
+            if (ok && elect_one()) scores(kb);
+        }
+        for (int kb = 0; ok && kb < nb; ++kb) {
+            const int at = kb % C::RING;
+            ok = wait_warp(&v_full[at], (kb / C::RING) & 1) && (kb + 2 >= nb || have_k(kb + 2)) &&
+                 (kb < scan0 || (wait_warp(&v_in[kb - scan0], 0) && wait_warp(&v_ok[kb - scan0], 0))) &&
+                 (kb >= mine || wait_warp(&p_full[i][kb & 1], (kb >> 1) & 1));
+            tc_fence_after();
+            if (ok && elect_one()) {
+                if (kb < mine) {
+                    const uint32_t v = smem_u32(ring_v + at * C::KT);
 #pragma unroll
                     for (int s = 0; s < BN / 16; ++s)
-                        umma_f16_tmem_a(tmem + C::O_COL + i * HD, tmem + i * BN + s * 8,
+                        umma_f16_tmem_a(tmem + C::O_COL + i * HD, tmem + (2 * i + (kb & 1)) * BN + s * 8,
                                         smem_desc_mn128(v + s * 2048, BN * 128, 1024), idesc_o, kb > 0 || s > 0);
-                    if (kb + 1 < mine) {
-                        next = true;
-                        ok = have(2 * kb + 2);
-                        if (!ok) break;
-                        scores(i, kb + 1);
-                        umma_commit(&s_full[i]);  // also: the tile's earlier products are done
-                    } else {
-                        umma_commit(&o_full[i]);
-                    }
+                    umma_commit(kb + 1 < mine ? &o_done[i] : &o_full[i]);
                 }
-                if (ok) umma_commit(&empty[(2 * kb + 1) % C::RING]);
-                if (ok && next) umma_commit(&empty[(2 * kb + 2) % C::RING]);
+                umma_commit(&v_empty[at]);
+                if (kb + 2 < nb) scores(kb + 2);  // over the scores of block kb: these products come first
             }
-            umma_commit(&drain);  // and all products are done
-            mbar_wait_bounded(&drain, 0, nullptr, p.timeout_ns);
         }
-    } else if (warp > NT * 4 + 1) {
+        if (elect_one()) umma_commit(&drain[i]);  // all products are done before the block ends
+        mbar_wait_bounded(&drain[i], 0, nullptr, p.timeout_ns);
+    } else if (warp > NT * 4 + NT) {
         // ---- scan of V
         constexpr uint32_t INF = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
-        const int me = tid - (NT * 4 + 2) * 32;
+        const int me = tid - (NT * 4 + NT + 1) * 32;
         for (int kb = scan0; kb < nb; ++kb) {
             if (!wait(&v_in[kb - scan0], 0)) break;
-            uint8_t* v = ring + (2 * kb + 1) % C::RING * C::KT;
-            for (int r = me; r < BN; r += 64) {
+            uint8_t* v = ring_v + kb % C::RING * C::KT;
+            for (int r = me; r < BN; r += C::SCAN) {
                 const int t = kb * BN + r;
                 uint32_t most = 0;
                 if (t < n) {
@@ -322,26 +281,38 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const int i = NT == 2 ? warp >> 2 : 0, row = tid & 127, q0 = q0_of(i), s = q0 + row;
         const int mine = i == 0 ? nb0 : nb1;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t S = tmem + lanes + i * BN, O = tmem + lanes + C::O_COL + i * HD;
+        const uint32_t S0 = tmem + lanes + 2 * i * BN, O = tmem + lanes + C::O_COL + i * HD;
         float m = -INFINITY, mc = 0.0f;  // the maximum that the exponentials refer to, and times c (0 for -infinity)
         uint64_t sum[4] = {0, 0, 0, 0};  // pairs of partial sums (+0.0)
         // TMEM is read and written by whole warps: their lanes give up together
         auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
         bool ok = true;
         for (int kb = 0; kb < mine; ++kb) {
-            ok = wait_warp(&s_full[i], kb & 1);
+            const uint32_t S = S0 + (kb & 1) * BN;
+            ok = wait_warp(&s_full[i][kb & 1], (kb >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
-            // S is read twice, 32 columns at a time with the next 32 on their way: a whole row does not
-            // fit in the registers beside the rest
-            const bool edge = kb >= q0 / BN;  // the same for the whole tile: TMEM is read by whole warps
-            const int see = s - kb * BN;      // keys up to here
-            const float mx = edge ? row_max<BN, true>(S, see) : row_max<BN, false>(S, see);
+            uint32_t x[BN];
+            tmem_ld_x32(S, x);
+            tmem_ld_x32(S + 32, x + 32);
+            tmem_wait_ld_regs(x);
+            tmem_wait_ld_regs(x + 32);
+            if (kb >= q0 / BN) {
+                const int see = s - kb * BN;  // keys up to here
+#pragma unroll
+                for (int e = 0; e < BN; ++e)
+                    if (e > see) x[e] = 0xff800000u;
+            }
+            const float mx = max_of<BN>(x);
             if (kb == 0) {
                 m = mx;
                 mc = m == -INFINITY ? 0.0f : m * a.c;
             } else if (__any_sync(0xffffffffu, (mx - m) * a.c > GROW)) {
-                // s_full says that the tile's earlier products are done: O is at rest
+                // O is at rest once the products of block kb - 1 are done; those of kb - 2 were before S,
+                // those of kb wait for this thread: the phase is the barrier's current or last one
+                ok = wait_warp(&o_done[i], (kb - 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
                 float by = 1.0f;
                 if ((mx - m) * a.c > GROW) {
                     by = m == -INFINITY ? 0.0f : exp2_fast(mc - mx * a.c);
@@ -359,11 +330,23 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     tmem_st_x32(O + 32 * h, o);
                 }
             }
-            if (edge) exponentials<T, BN, true>(S, a.c, mc, see, sum);
-            else exponentials<T, BN, false>(S, a.c, mc, see, sum);
+            const uint64_t c2 = two(a.c, a.c), m2 = two(-mc, -mc);
+#pragma unroll
+            for (int h = 0; h < BN / 32; ++h) {
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const uint32_t* y = x + 32 * h + 2 * e;
+                    const float2 z = one_by_one(fma2(two(__uint_as_float(y[0]), __uint_as_float(y[1])), c2, m2));
+                    const float e0 = exp2_fast(z.x), e1 = exp2_fast(z.y);
+                    sum[e & 3] = add2(sum[e & 3], two(e0, e1));
+                    w[e] = pack2<T>(e0, e1);
+                }
+                tmem_st_x16(S + 16 * h, w);
+            }
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(&p_full[i]);
+            mbar_arrive(&p_full[i][kb & 1]);
         }
         if (mine > 0 && ok) ok = wait_warp(&o_full[i], 0);
         // values that are not finite, as noted for the blocks that this tile reads
@@ -456,8 +439,8 @@ static cudaError_t prompt_tc(const PromptArgs& p, cudaStream_t st) {
     CUtensorMap q, k, v, o;
     const int64_t wq = (int64_t)p.n_heads * HD, wk = (int64_t)p.n_kv * HD;
     cudaError_t e = rows_map(&q, p.dtype, p.q, wq, p.rows, p.ld_q, BM);
-    if (e == cudaSuccess) e = rows_map(&k, p.dtype, p.k, wk, p.rows, p.ld_k, C::BN);
-    if (e == cudaSuccess) e = rows_map(&v, p.dtype, p.v, wk, p.rows, p.ld_v, C::BN);
+    if (e == cudaSuccess) e = rows_map(&k, p.dtype, p.k, wk, p.rows, p.ld_k, BN);
+    if (e == cudaSuccess) e = rows_map(&v, p.dtype, p.v, wk, p.rows, p.ld_v, BN);
     if (e == cudaSuccess) e = rows_map(&o, p.dtype, p.o, wq, p.rows, p.ld_o, BM);
     if (e == cudaSuccess) e = prepare_smem((const void*)prompt_tc_kernel<T, HD, NT>, C::SMEM);
     if (e != cudaSuccess) return e;

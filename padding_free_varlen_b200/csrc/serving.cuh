@@ -84,6 +84,18 @@ __device__ __forceinline__ bool wait_in_line(uint64_t* bar, uint32_t parity, con
     return false;
 }
 
+// One lane of a converged warp, the same one each time.  Work that a single thread issues is issued
+// by a warp whose control flow is uniform: its operands then live in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ uint64_t two(float lo, float hi) {
     uint64_t r;
