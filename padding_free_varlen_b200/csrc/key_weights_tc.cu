@@ -26,7 +26,8 @@ namespace {
 constexpr int BK = 128;            // keys per block
 constexpr int BQ = 128;            // queries per step
 constexpr int BOX = 128 * 128;     // bytes of 128 rows x 64 columns of 16 bits
-constexpr int THREADS = 128 + 96;  // a thread per key; loader, products, sums
+constexpr int EXP_WARPS = 8;       // two threads per key, each with half of a step's queries
+constexpr int THREADS = EXP_WARPS * 32 + 96;  // and loader, products, sums
 constexpr float LOG2E = 1.4426950408889634f;
 
 template <int HD>
@@ -36,13 +37,13 @@ struct WCfg {
 };
 }  // namespace
 
-// Adds the exponentials of 64 columns of a key's row; with EDGE only columns lo .. hi - 1 count.
+// Adds the exponentials of 32 columns of a key's row; with EDGE only columns lo .. hi - 1 count.
 template <bool EDGE>
 __device__ __forceinline__ void add_exponentials(const uint32_t* r, const float* neg_lse, uint64_t c2, int lo, int hi,
                                                  uint64_t (&sum)[2]) {
     const float4* l4 = reinterpret_cast<const float4*>(neg_lse);
 #pragma unroll
-    for (int e = 0; e < 64; e += 4) {
+    for (int e = 0; e < 32; e += 4) {
         const float4 l = l4[e / 4];
         float2 u = one_by_one(fma2(two(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), c2, two(l.x, l.y)));
         float2 v = one_by_one(fma2(two(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])), c2, two(l.z, l.w)));
@@ -73,9 +74,9 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     __shared__ uint32_t tmem_slot;
     __shared__ int dead;
     __shared__ __align__(16) float neg_lse[2][BQ];  // -lse in units of log2
-    __shared__ float part[BK];
+    __shared__ float part[2][BK];
     const PromptArgs& p = a.p;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     // blocks of a cluster share the item; items of all kv heads pass by before the next tile of keys
     const int64_t lin = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) / a.cluster;
     const int rank = blockIdx.x % a.cluster, kvh = (int)(lin % p.n_kv);
@@ -98,29 +99,31 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     if (tid == 0) {
         mbar_init(&k_full, 1), mbar_init(&drain, 1);
         for (int i = 0; i < 2; ++i)
-            mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 1), mbar_init(&l_full[i], 32), mbar_init(&s_full[i], 1), mbar_init(&s_empty[i], 128);
+            mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 1), mbar_init(&l_full[i], 32), mbar_init(&s_full[i], 1), mbar_init(&s_empty[i], EXP_WARPS * 32);
         dead = stopped(p.status);  // the blocks of a cluster must not part: no early return
         fence_mbar_init();
     }
-    if (warp == 4) {
+    if (warp == EXP_WARPS) {
         tmem_alloc(&tmem_slot, 2 * BQ);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
     const bool was_stopped = dead != 0;
     __syncthreads();
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (mbar_wait_bounded(bar, parity, &dead, p.timeout_ns)) return true;
+        if (wait_in_line(bar, parity, &dead, p.timeout_ns)) return true;
         *reinterpret_cast<volatile int*>(&dead) = 1;
         return false;
     };
+    // TMEM is read, and work is issued, by whole warps: their lanes give up together
+    auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
 
     if (was_stopped) {
         // no work
-    } else if (warp == 4) {
+    } else if (warp == EXP_WARPS) {
         if (lane == 0) {
             // ---- loader
             mbar_arrive_expect_tx(&k_full, C::TILE);
@@ -137,15 +140,14 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             mbar_wait_bounded(&k_full, 0, nullptr, p.timeout_ns);
             for (int y = max(0, x - 2); y < x; ++y) mbar_wait_bounded(&q_full[y & 1], (y >> 1) & 1, nullptr, p.timeout_ns);
         }
-    } else if (warp == 5) {
-        if (lane == 0) {
-            // ---- products
-            constexpr uint32_t idesc = idesc_f16(std::is_same<T, __half>::value ? 0u : 1u, BK, BQ, 0);
-            bool ok = wait(&k_full, 0);
-            for (int x = 0; ok && x < steps; ++x) {
-                ok = wait(&q_full[x & 1], (x >> 1) & 1) && (x < 2 || wait(&s_empty[x & 1], ((x >> 1) - 1) & 1));
-                if (!ok) break;
-                tc_fence_after();
+    } else if (warp == EXP_WARPS + 1) {
+        // ---- products: the whole warp follows, one lane issues
+        constexpr uint32_t idesc = idesc_f16(std::is_same<T, __half>::value ? 0u : 1u, BK, BQ, 0);
+        bool ok = wait_warp(&k_full, 0);
+        for (int x = 0; ok && x < steps; ++x) {
+            ok = wait_warp(&q_full[x & 1], (x >> 1) & 1) && (x < 2 || wait_warp(&s_empty[x & 1], ((x >> 1) - 1) & 1));
+            tc_fence_after();
+            if (ok && elect_one()) {
                 const uint32_t k = smem_u32(base), q = smem_u32(sq + (x & 1) * C::TILE);
 #pragma unroll
                 for (int s = 0; s < HD / 16; ++s)
@@ -154,10 +156,10 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 umma_commit(&s_full[x & 1]);
                 umma_commit(&q_empty[x & 1]);
             }
-            umma_commit(&drain);  // all products are done before the block ends
-            mbar_wait_bounded(&drain, 0, nullptr, p.timeout_ns);
         }
-    } else if (warp == 6) {
+        if (elect_one()) umma_commit(&drain);  // all products are done before the block ends
+        mbar_wait_bounded(&drain, 0, nullptr, p.timeout_ns);
+    } else if (warp == EXP_WARPS + 2) {
         // ---- sums of the queries
         for (int x = 0; x < steps; ++x) {
             if (x >= 2 && !wait(&s_empty[x & 1], ((x >> 1) - 1) & 1)) break;
@@ -171,43 +173,45 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             mbar_arrive(&l_full[x & 1]);
         }
     } else {
-        // ---- exponentials, one key per thread
-        const int t = t0 + tid;
-        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        // ---- exponentials
+        const int half = warp >> 2, t = t0 + (tid & 127);
+        const uint32_t S = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * (BQ / 2);
         const uint64_t c2 = two(a.c, a.c);
         uint64_t sum[2] = {two(0.0f, 0.0f), two(0.0f, 0.0f)};
         for (int x = 0; x < steps; ++x) {
             const int at = x & 1;
-            const bool ok = wait(&l_full[at], (x >> 1) & 1) && wait(&s_full[at], (x >> 1) & 1);
-            if (!__all_sync(0xffffffffu, ok)) break;  // TMEM is read by whole warps
+            if (!wait_warp(&l_full[at], (x >> 1) & 1) || !wait_warp(&s_full[at], (x >> 1) & 1)) break;
             tc_fence_after();
-            const int s0 = begin + x % per_head * BQ;
-            const bool edge = s0 < t0 + BK - 1 || s0 + BQ > n;
-            const int lo = t - s0, hi = n - s0;  // queries lo .. hi - 1 of the tile see this key
+            const int s0 = begin + x % per_head * BQ + half * (BQ / 2);
+            const bool edge = s0 < t0 + BK - 1 || s0 + BQ / 2 > n;
+            const int lo = t - s0, hi = n - s0;  // queries lo .. hi - 1 of these 64 see this key
+            if (hi > 0) {
+                uint32_t r[2][32];
+                tmem_ld_x32(S + at * BQ, r[0]);
+                tmem_ld_x32(S + at * BQ + 32, r[1]);
+                tmem_wait_ld_regs(r[0]);
+                tmem_wait_ld_regs(r[1]);
 #pragma unroll
-            for (int h = 0; h < BQ / 64; ++h) {
-                uint32_t r[64];
-                tmem_ld_x32(tmem + lanes + at * BQ + 64 * h, r);
-                tmem_ld_x32(tmem + lanes + at * BQ + 64 * h + 32, r + 32);
-                tmem_wait_ld_regs(r);
-                tmem_wait_ld_regs(r + 32);
-                if (64 * h >= hi) break;
-                if (edge) add_exponentials<true>(r, &neg_lse[at][64 * h], c2, lo - 64 * h, hi - 64 * h, sum);
-                else add_exponentials<false>(r, &neg_lse[at][64 * h], c2, 0, 0, sum);
+                for (int h = 0; h < 2; ++h) {
+                    const float* l = &neg_lse[at][half * (BQ / 2) + 32 * h];
+                    if (edge) add_exponentials<true>(r[h], l, c2, lo - 32 * h, hi - 32 * h, sum);
+                    else add_exponentials<false>(r[h], l, c2, 0, 0, sum);
+                }
             }
             tc_fence_before();
             mbar_arrive(&s_empty[at]);
         }
         const float2 u = one_by_one(add2(sum[0], sum[1]));
-        part[tid] = u.x + u.y;
+        part[half][tid & 127] = u.x + u.y;
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 4) tmem_dealloc(tmem, 2 * BQ);
+    if (warp == EXP_WARPS) tmem_dealloc(tmem, 2 * BQ);
     if (tid == 0 && dead) status_or(p.status, ENERGON_DEVICE_TIMEOUT);
-    float w = tid < BK ? part[tid] : 0.0f;
+    if (tid < BK) part[0][tid] += part[1][tid];
+    float w = tid < BK ? part[0][tid] : 0.0f;
     bool good = dead == 0;
     if (a.cluster > 1) {
         cluster_sync();
@@ -216,7 +220,7 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             for (int r = 0; r < a.cluster; ++r) {
                 float y;
                 int d;
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(y) : "r"(mapa_shared(smem_u32(&part[tid]), r)) : "memory");
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(y) : "r"(mapa_shared(smem_u32(&part[0][tid]), r)) : "memory");
                 asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(d) : "r"(mapa_shared(smem_u32(&dead), r)) : "memory");
                 w += y;
                 good = good && d == 0;
