@@ -28,6 +28,9 @@ constexpr int BQ = 128;            // queries per step
 constexpr int BOX = 128 * 128;     // bytes of 128 rows x 64 columns of 16 bits
 constexpr int EXP_WARPS = 8;       // two threads per key, each with half of a step's queries
 constexpr int THREADS = EXP_WARPS * 32 + 96;  // and loader, products, sums
+// One pair of columns in four takes its exponentials from the FMA pipe (2^x by a polynomial): 103 us
+// on one prompt of 4096 tokens with 32 heads, against 110 us with none and 112 us with every second.
+constexpr int POLY = 8;
 constexpr float LOG2E = 1.4426950408889634f;
 
 template <int HD>
@@ -54,7 +57,8 @@ __device__ __forceinline__ void add_exponentials(const uint32_t* r, const float*
             if (e + 3 < lo || e + 3 >= hi) v.y = -INFINITY;
         }
         sum[0] = add2(sum[0], two(exp2_fast(u.x), exp2_fast(u.y)));
-        sum[1] = add2(sum[1], two(exp2_fast(v.x), exp2_fast(v.y)));
+        v = e % POLY == 0 ? exp2_poly<5>(v) : make_float2(exp2_fast(v.x), exp2_fast(v.y));
+        sum[1] = add2(sum[1], two(v.x, v.y));
     }
 }
 
