@@ -28,13 +28,14 @@ namespace energon {
 namespace {
 constexpr int STEP = 32;     // tokens a warp takes at a time
 constexpr int CW = 4;        // warps per block
-constexpr int STAGES = 3;    // buffers per warp
+constexpr int STAGES = 2;    // buffers per warp
 constexpr int BLOCK_STEP = STEP * CW;
 constexpr int MAX_SPLITS = 148;
 constexpr int SUPER = 32;    // steps whose page entries a warp holds (one per lane)
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
-constexpr float P_UP = 16384.0f;  // 2^14: keeps small probabilities in the normal range of fp16
+constexpr float GROW = 8.0f;      // log2 of the growth that a running maximum may lag behind
+constexpr float P_UP = 128.0f;    // 2^7: the exponentials, at most 2^GROW, fill the range of fp16
 
 template <int HD>
 struct DCfg {
@@ -43,10 +44,9 @@ struct DCfg {
     static constexpr int SMEM = CW * WARP + 1024;
 };
 
-// What a call keeps between its launches: per (sequence, head) log2 of the sum; per split a
-// maximum and sum and an unnormalised output; the scores (accumulate only).
+// What a call keeps between its launches: per split a maximum and sum, with more than one split an
+// unnormalised output; the scores (accumulate only).
 struct AttnWs {
-    float* lse2;    // [batch][heads]
     float2* ml;     // [batch][heads][splits]
     float* part;    // [batch][heads][splits][d]
     float* scores;  // [batch][heads][stride], in units of log2
@@ -76,9 +76,8 @@ AttnWs attn_ws(void* ws, int batch, int max_len, int n_heads, int n_kv, int head
         at += (n + 255) / 256 * 256;
         return p;
     };
-    w.lse2 = reinterpret_cast<float*>(take(rows * sizeof(float)));
     const size_t parts = w.splits > 1 ? (size_t)rows * w.splits : 0;
-    w.ml = reinterpret_cast<float2*>(take(parts * sizeof(float2)));
+    w.ml = reinterpret_cast<float2*>(take((size_t)rows * w.splits * sizeof(float2)));
     w.part = reinterpret_cast<float*>(take(parts * head_dim * sizeof(float)));
     w.scores = reinterpret_cast<float*>(take(accumulate ? (size_t)rows * w.stride * sizeof(float) : 0));
     w.bytes = at;
@@ -227,6 +226,10 @@ __global__ void __launch_bounds__(CW * 32) cache_attn_kernel(const __grid_consta
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[r][i][e] = 0.0f;
     }
+    float* scores[R];      // this lane's rows of the scores (accumulate only)
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        scores[r] = sp.ws.scores + ((int64_t)b * a.n_heads + head0 + g + 8 * r) * sp.ws.stride + 2 * cc;
     float v_most = 0.0f;  // largest value scale met: the unit of acc
     bool ok = true;
     uint8_t* mine = ring + warp * C::WARP;
@@ -336,48 +339,56 @@ __global__ void __launch_bounds__(CW * 32) cache_attn_kernel(const __grid_consta
                     }
                 }
 
-            // scores in units of log2, masked; new maxima
+            // scores in units of log2, masked; the maxima that the exponentials refer to
             const int p0 = __shfl_sync(0xffffffffu, page[0], i), p1 = __shfl_sync(0xffffffffu, page[1], i);
             const float ks0 = __shfl_sync(0xffffffffu, ks[0], i), ks1 = __shfl_sync(0xffffffffu, ks[1], i);
             const float vs0 = __shfl_sync(0xffffffffu, vs[0], i), vs1 = __shfl_sync(0xffffffffu, vs[1], i);
-            float alpha[R];
-            bool moved = false;
+            const bool whole = t0 + STEP <= t_end && p0 >= 0 && p1 >= 0;
+            float mx[R];
+            bool grown = false;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                float mx = -INFINITY;
+                const float f0 = ks0 * qs[r], f1 = ks1 * qs[r];
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const bool there = (u ? p1 : p0) >= 0;
+                for (int u = 0; u < 2; ++u)
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float& y = x[u][j][2 * r + e];
-                            y = there && t0 + 16 * u + 8 * j + 2 * cc + e < t_end ? y * (u ? ks1 : ks0) * qs[r] : -INFINITY;
-                            mx = fmaxf(mx, y);
-                        }
-                }
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float m_new = fmaxf(m[r], mx);
-                moved |= m_new > m[r];
-                alpha[r] = m[r] == -INFINITY ? 0.0f : exp2f(m[r] - m_new);
-                m[r] = m_new;
-                if (a.accumulate && g + 8 * r < n_q) {
-                    float* to = sp.ws.scores + ((int64_t)b * a.n_heads + head0 + g + 8 * r) * sp.ws.stride + t0 + 2 * cc;
+                        for (int e = 0; e < 2; ++e) x[u][j][2 * r + e] *= u ? f1 : f0;
+                if (!whole) {
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
-                            if (t0 + 16 * u + 8 * j + 2 * cc < t_end)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                if ((u ? p1 : p0) < 0 || t0 + 16 * u + 8 * j + 2 * cc + e >= t_end) x[u][j][2 * r + e] = -INFINITY;
+                }
+                mx[r] = max3(fmaxf(x[0][0][2 * r], x[0][0][2 * r + 1]), x[0][1][2 * r], x[0][1][2 * r + 1]);
+                mx[r] = max3(max3(mx[r], x[1][0][2 * r], x[1][0][2 * r + 1]), x[1][1][2 * r], x[1][1][2 * r + 1]);
+                mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+                mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+                grown |= mx[r] - m[r] > GROW;
+                if (a.accumulate && g + 8 * r < n_q) {
+                    float* to = scores[r] + t0;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            if (whole || t0 + 16 * u + 8 * j + 2 * cc < t_end)
                                 *reinterpret_cast<float2*>(to + 16 * u + 8 * j) = make_float2(x[u][j][2 * r], x[u][j][2 * r + 1]);
                 }
             }
-            if (__any_sync(0xffffffffu, moved)) {
+            if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    l[r] *= alpha[r];
-                    const float f0 = __shfl_sync(0xffffffffu, alpha[r], 8 * cc), f1 = __shfl_sync(0xffffffffu, alpha[r], 8 * cc + 4);
+                    float alpha = 1.0f;
+                    if (mx[r] - m[r] > GROW) {
+                        alpha = m[r] == -INFINITY ? 0.0f : exp2_fast(m[r] - mx[r]);
+                        m[r] = mx[r];
+                    }
+                    l[r] *= alpha;
+                    const float f0 = __shfl_sync(0xffffffffu, alpha, 8 * cc), f1 = __shfl_sync(0xffffffffu, alpha, 8 * cc + 4);
 #pragma unroll
                     for (int y = 0; y < ND / 2; ++y)
                         acc[r][y][0] *= f0, acc[r][y][1] *= f1, acc[r][y][2] *= f0, acc[r][y][3] *= f1;
@@ -392,7 +403,7 @@ __global__ void __launch_bounds__(CW * 32) cache_attn_kernel(const __grid_consta
                     const float ms = m[r] == -INFINITY ? 0.0f : m[r];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const float e0 = exp2f(x[u][j][2 * r] - ms), e1 = exp2f(x[u][j][2 * r + 1] - ms);
+                        const float e0 = exp2_fast(x[u][j][2 * r] - ms), e1 = exp2_fast(x[u][j][2 * r + 1] - ms);
                         l[r] += e0 + e1;
                         pf[0][r][j] = pair_f16(e0 * vf, e1 * vf);
                         if constexpr (TERMS == 2) pf[1][r][j] = rest_f16(e0 * vf, e1 * vf, pf[0][r][j]);
@@ -475,75 +486,112 @@ __global__ void __launch_bounds__(CW * 32) cache_attn_kernel(const __grid_consta
             o += out[(w * QT + q) * LD + d];
         }
         const int64_t row = (int64_t)b * a.n_heads + head0 + q;
+        if (d == 0) sp.ws.ml[row * sp.ws.splits + split] = make_float2(top, sum);
         if (sp.ws.splits > 1) {
             sp.ws.part[(row * sp.ws.splits + split) * HD + d] = o;
-            if (d == 0) sp.ws.ml[row * sp.ws.splits + split] = make_float2(top, sum);
         } else {
             static_cast<T*>(a.o)[b * a.ld_o + (int64_t)(head0 + q) * HD + d] = from_f<T>(sum == 0.0f ? 0.0f : o / sum);
             if (d == 0) {
-                sp.ws.lse2[row] = sum == 0.0f ? -INFINITY : top + log2f(sum);
                 if (a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : top * LN2 + logf(sum);
             }
         }
     }
 }
 
-// The splits of one (sequence, query head) joined: one thread per output.
+// What remains when the splits are done, per (sequence, kv head).  With more than one split the first
+// blocks join the outputs of one query head each; the others add the probabilities of 1024 tokens to
+// their weights,
+//     weight(t) += sum over the heads of the group of exp2(score - lse).
+constexpr int FIN = 256;
 template <typename T, int HD>
-__global__ void __launch_bounds__(HD) cache_join_kernel(const CacheAttnArgs a, const AttnWs ws) {
+__global__ void __launch_bounds__(FIN) cache_finish_kernel(const CacheAttnArgs a, const AttnWs ws) {
     const CacheArgs& c = a.c;
-    __shared__ float f[MAX_SPLITS], sum;
-    let_next_grid_start();
     wait_for_earlier_grid();
     if (stopped(c.status)) return;
-    const int head = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+    const int b = blockIdx.z, kvh = blockIdx.y, group = a.n_heads / c.n_kv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     bool bad;
     const int n = cached_len(c, b, bad);
     const int live = max(1, (n + ws.chunk - 1) / ws.chunk);
-    const int64_t row = (int64_t)b * a.n_heads + head;
-    if (tid < 32) {
-        float top = -INFINITY;
-        for (int s = tid; s < live; s += 32) top = fmaxf(top, ws.ml[row * ws.splits + s].x);
-        top = warp_max(top);
-        float l = 0.0f;
-        for (int s = tid; s < live; s += 32) {
-            const float2 ml = ws.ml[row * ws.splits + s];
-            f[s] = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - top);
-            l += ml.x == -INFINITY ? 0.0f : ml.y * f[s];
+    const int64_t row0 = (int64_t)b * a.n_heads + kvh * group;
+    const int joins = ws.splits > 1 ? group : 0;
+    if ((int)blockIdx.x < joins) {
+        __shared__ float f[MAX_SPLITS], sums[FIN / 32][HD], total;
+        const int64_t row = row0 + blockIdx.x;
+        if (warp == 0) {
+            float top = -INFINITY, l = 0.0f;
+            for (int s = lane; s < live; s += 32) top = fmaxf(top, ws.ml[row * ws.splits + s].x);
+            top = warp_max(top);
+            for (int s = lane; s < live; s += 32) {
+                const float2 ml = ws.ml[row * ws.splits + s];
+                f[s] = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - top);
+                l += ml.x == -INFINITY ? 0.0f : ml.y * f[s];
+            }
+            l = warp_sum(l);
+            if (lane == 0) {
+                total = l;
+                if (a.lse) a.lse[row] = l == 0.0f ? -INFINITY : top * LN2 + logf(l);
+            }
         }
-        l = warp_sum(l);
-        if (tid == 0) {
-            sum = l;
-            ws.lse2[row] = l == 0.0f ? -INFINITY : top + log2f(l);
-            if (a.lse) a.lse[row] = l == 0.0f ? -INFINITY : top * LN2 + logf(l);
+        __syncthreads();
+        const float* part = ws.part + row * ws.splits * HD + lane * (HD / 32);
+        float o[HD / 32] = {};
+#pragma unroll 4
+        for (int s = warp; s < live; s += FIN / 32) {
+            const float w = f[s];
+#pragma unroll
+            for (int e = 0; e < HD / 32; ++e) o[e] += part[(int64_t)s * HD + e] * w;
         }
+#pragma unroll
+        for (int e = 0; e < HD / 32; ++e) sums[warp][lane * (HD / 32) + e] = o[e];
+        __syncthreads();
+        if (tid < HD) {
+            float y = 0.0f;
+#pragma unroll
+            for (int w = 0; w < FIN / 32; ++w) y += sums[w][tid];
+            static_cast<T*>(a.o)[b * a.ld_o + (int64_t)(kvh * group + blockIdx.x) * HD + tid] = from_f<T>(total == 0.0f ? 0.0f : y / total);
+        }
+        return;
     }
-    __syncthreads();
-    const float* part = ws.part + row * ws.splits * HD + tid;
-    float o = 0.0f;
+    const int t0 = ((int)blockIdx.x - joins) * 4 * FIN;
+    if (t0 >= n) return;
+    const int t = t0 + 4 * tid;
+    int page = -1;
+    if (t < n) page = c.table[(int64_t)b * c.max_pages + t / c.page_len];  // 4 tokens never cross a page
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    __shared__ float lse2[64];
+    for (int h0 = 0; h0 < group; h0 += 64) {
+        const int some = min(64, group - h0);
+        __syncthreads();
+        for (int h = warp; h < some; h += FIN / 32) {  // the sums of the heads over the splits
+            const int64_t row = row0 + h0 + h;
+            float top = -INFINITY, l = 0.0f;
+            for (int s = lane; s < live; s += 32) top = fmaxf(top, ws.ml[row * ws.splits + s].x);
+            top = warp_max(top);
+            for (int s = lane; s < live; s += 32) {
+                const float2 ml = ws.ml[row * ws.splits + s];
+                l += ml.x == -INFINITY ? 0.0f : ml.y * exp2f(ml.x - top);
+            }
+            l = warp_sum(l);
+            if (lane == 0) lse2[h] = top + log2f(l);
+        }
+        __syncthreads();
+        if ((unsigned)page < (unsigned)c.n_pages) {
+            const float* x = ws.scores + (row0 + h0) * ws.stride + t;
 #pragma unroll 8
-    for (int s = 0; s < live; ++s) o += part[(int64_t)s * HD] * f[s];
-    static_cast<T*>(a.o)[b * a.ld_o + (int64_t)head * HD + tid] = from_f<T>(sum == 0.0f ? 0.0f : o / sum);
-}
-
-// weight(t) += sum over the heads of the group of exp2(score - lse)
-__global__ void __launch_bounds__(256) cache_weight_kernel(const CacheAttnArgs a, const AttnWs ws) {
-    const CacheArgs& c = a.c;
-    wait_for_earlier_grid();
-    if (stopped(c.status)) return;
-    const int b = blockIdx.z, kvh = blockIdx.y, group = a.n_heads / c.n_kv, P = c.page_len;
-    bool bad;
-    const int n = cached_len(c, b, bad), t = blockIdx.x * 256 + threadIdx.x;
-    if (t >= n) return;
-    const int page = c.table[(int64_t)b * c.max_pages + t / P];
-    if ((unsigned)page >= (unsigned)c.n_pages) return;
-    float sum = 0.0f;
-    for (int g = 0; g < group; ++g) {
-        const int64_t r = (int64_t)b * a.n_heads + kvh * group + g;
-        sum += exp2f(ws.scores[r * ws.stride + t] - ws.lse2[r]);
+            for (int h = 0; h < some; ++h) {
+                const float4 y = *reinterpret_cast<const float4*>(x + (int64_t)h * ws.stride);
+                const float z = lse2[h];
+                sum.x += exp2f(y.x - z), sum.y += exp2f(y.y - z), sum.z += exp2f(y.z - z), sum.w += exp2f(y.w - z);
+            }
+        }
     }
+    if ((unsigned)page >= (unsigned)c.n_pages) return;
     // a page of one sequence has one writer per call; sequences that share a page add in any order
-    atomicAdd(c.weight + ((int64_t)page * c.n_kv + kvh) * P + t % P, sum);
+    float* w = c.weight + ((int64_t)page * c.n_kv + kvh) * c.page_len + t % c.page_len;
+    atomicAdd(w, sum.x);
+    if (t + 1 < n) atomicAdd(w + 1, sum.y);
+    if (t + 2 < n) atomicAdd(w + 2, sum.z);
+    if (t + 3 < n) atomicAdd(w + 3, sum.w);
 }
 
 size_t cache_attention_ws_bytes(int batch, int max_len, int n_heads, int n_kv, int head_dim, bool accumulate) {
@@ -591,10 +639,9 @@ static cudaError_t cache_attn(const CacheAttnArgs& a, cudaStream_t st) {
     const dim3 grid(sp.ws.splits, a.c.n_kv * sp.q_tiles, a.c.batch);
     cache_attn_kernel<T, HD, QT><<<grid, CW * 32, DCfg<HD>::SMEM, st>>>(tm_k, tm_v, a, sp);
     e = cudaGetLastError();
-    if (e == cudaSuccess && sp.ws.splits > 1)
-        e = launch_early(cache_join_kernel<T, HD>, dim3(a.n_heads, a.c.batch), HD, st, a, sp.ws);
-    if (e == cudaSuccess && a.accumulate && a.c.max_len > 0)
-        e = launch_early(cache_weight_kernel, dim3(cdiv(a.c.max_len, 256), a.c.n_kv, a.c.batch), 256, st, a, sp.ws);
+    const int finish = (sp.ws.splits > 1 ? a.n_heads / a.c.n_kv : 0) + (a.accumulate ? cdiv(a.c.max_len, 4 * FIN) : 0);
+    if (e == cudaSuccess && finish > 0)
+        e = launch_early(cache_finish_kernel<T, HD>, dim3(finish, a.c.n_kv, a.c.batch), FIN, st, a, sp.ws);
     return e;
 }
 
