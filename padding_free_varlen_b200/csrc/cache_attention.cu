@@ -49,8 +49,8 @@ struct DCfg {
 struct AttnWs {
     float2* ml;     // [batch][heads][splits]
     float* part;    // [batch][heads][splits][d]
-    float* scores;  // [batch][heads][stride], in units of log2
-    int stride, splits, chunk;
+    float* scores;  // [batch][kv heads][stride][group], in units of log2
+    int stride, splits, chunk, group;  // group: query heads per kv head
     size_t bytes;
 };
 inline int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
@@ -69,6 +69,7 @@ AttnWs attn_ws(void* ws, int batch, int max_len, int n_heads, int n_kv, int head
     w.chunk = cdiv(cdiv(max_len > 0 ? max_len : 1, want), BLOCK_STEP) * BLOCK_STEP;
     w.splits = cdiv(max_len > 0 ? max_len : 1, w.chunk);
     w.stride = cdiv(max_len, 16) * 16;
+    w.group = n_heads / n_kv;
     size_t at = 0;
     char* base = static_cast<char*>(ws);
     auto take = [&](size_t n) {
@@ -97,6 +98,21 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same with a zero sum before it.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+// An 8 x 8 matrix of 16-bit elements (lane 4 g + c: row g, columns 2c and 2c + 1) transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
 // Two biased codes (bytes LO and HI of w, each code + 128) as a pair of fp16: 0x6400 | byte is
 // 1024 + byte, less 1152.
 template <int LO, int HI>
@@ -106,6 +122,8 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t w) {
     const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&x), bias);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
+// 2^k for -126 <= k <= 127.
+__device__ __forceinline__ float power_of_two(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
 __device__ __forceinline__ uint32_t pair_f16(float a, float b) { return pack2<__half>(a, b); }
 // What fp16 leaves of a pair.
 __device__ __forceinline__ uint32_t rest_f16(float a, float b, uint32_t hi) {
@@ -148,12 +166,14 @@ struct SplitArgs {
 };
 
 // One block = one split of one sequence, for up to QT query heads of one kv head.  Fragment
-// layout of a warp's lane (g = lane / 4, c = lane % 4): in the scores g is the query and tokens
-// 2c, 2c + 1 of each 8 are the columns; the contraction over d takes the elements of lane c from
-// its own d / 4 consecutive ones, for queries and keys alike.  The output is held transposed, rows
-// d = (d / 8) g + j, columns queries 2c, 2c + 1, so that the probabilities need no exchange.
+// layout of a warp's lane (g = lane / 4, c = lane % 4): scores have tokens g, g + 8 of each 16 as
+// rows and queries 2c, 2c + 1 (+ 8 r) as columns; the contraction over d takes the elements of lane
+// c from its own d / 4 consecutive ones, for queries and keys alike.  The output is held transposed,
+// rows d = (d / 8) g + j, columns queries 2c, 2c + 1: the lane that holds a query's maximum and sum
+// also holds its outputs, and the probabilities become the second product's operand by
+// transposing 8 x 8 blocks.
 template <typename T, int HD, int QT>
-__global__ void __launch_bounds__(CW * 32) cache_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
+__global__ void __launch_bounds__(CW * 32, QT == 8 && sizeof(T) == 2 ? 3 : 2) cache_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
                                                              const __grid_constant__ CUtensorMap tm_v,
                                                              const CacheAttnArgs a, const SplitArgs sp) {
     using C = DCfg<HD>;
@@ -188,7 +208,7 @@ __global__ void __launch_bounds__(CW * 32) cache_attn_kernel(const __grid_consta
 
     // this lane's part of the queries
     uint32_t qf[TERMS][KS][R][2];
-    float qs[R];
+    float qs[R][2];  // of queries 8 r + 2c, + 1
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         float x[HD / 4], most = 0.0f;
@@ -203,52 +223,62 @@ __global__ void __launch_bounds__(CW * 32) cache_attn_kernel(const __grid_consta
         for (int i = 0; i < HD / 4; ++i) most = fmaxf(most, fabsf(x[i]));
         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-        int e = 0;
-        if (isinf(most)) e = 129;
-        else if (most > 0.0f) frexpf(most, &e);
-        qs[r] = ldexpf(a.scale * LOG2E, e - 15);
+        // most < 2^e; what lies below the normal range is held to 2^-149
+        const int e = most > 0.0f ? max((int)(__float_as_uint(most) >> 23), 1) - 126 : 0;
+        const float q_unit = ldexpf(a.scale * LOG2E, e - 15);
+        qs[r][0] = __shfl_sync(0xffffffffu, q_unit, 8 * cc), qs[r][1] = __shfl_sync(0xffffffffu, q_unit, 8 * cc + 4);
+        // 2^(15 - e) in two factors: alone it may lie outside the range of fp32
+        const float up0 = power_of_two((15 - e) / 2), up1 = power_of_two(15 - e - (15 - e) / 2);
 #pragma unroll
         for (int s = 0; s < KS; ++s)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float u = ldexpf(x[4 * s + 2 * h], 15 - e), v = ldexpf(x[4 * s + 2 * h + 1], 15 - e);
+                const float u = x[4 * s + 2 * h] * up0 * up1, v = x[4 * s + 2 * h + 1] * up0 * up1;
                 qf[0][s][r][h] = pair_f16(u, v);
                 if constexpr (TERMS == 2) qf[1][s][r][h] = rest_f16(u, v, qf[0][s][r][h]);
             }
     }
 
-    float m[R], l[R], acc[R][ND / 2][4];
+    float m[R][2], l[R][2], acc[R][ND / 2][4];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        m[r] = -INFINITY, l[r] = 0.0f;
+        m[r][0] = m[r][1] = -INFINITY, l[r][0] = l[r][1] = 0.0f;
 #pragma unroll
         for (int i = 0; i < ND / 2; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[r][i][e] = 0.0f;
     }
-    float* scores[R];      // this lane's rows of the scores (accumulate only)
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-        scores[r] = sp.ws.scores + ((int64_t)b * a.n_heads + head0 + g + 8 * r) * sp.ws.stride + 2 * cc;
+    // scores are kept as [token][query of the group]; this lane's place for its sequence's token g
+    float* const scores = sp.ws.scores + (((int64_t)b * c.n_kv + kvh) * sp.ws.stride + g) * sp.ws.group + qt * QT + 2 * cc;
+    const int log_p = __ffs(P) - 1;
     float v_most = 0.0f;  // largest value scale met: the unit of acc
     bool ok = true;
     uint8_t* mine = ring + warp * C::WARP;
+    // Where this lane's pieces begin in a buffer: keys of token g (16-byte pieces 2c and 2c + 1, or c), values
+    // of tokens 2c and 2c + 1 (piece g, or half of piece g / 2).  The swizzle repeats after 8 rows.
+    const int k_at[2] = {g * HD + ((HD == 128 ? (2 * cc) ^ g : cc ^ ((g >> 1) & 3)) << 4), g * HD + (((2 * cc + 1) ^ g) << 4)};
+    int v_at[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int row = 2 * cc + h;
+        v_at[h] = C::TILE + row * HD + (HD == 128 ? (g ^ row) << 4 : (((g >> 1) ^ ((row >> 1) & 3)) << 4) + 8 * (g & 1));
+    }
     const int total = max(0, (t_end - t_begin + STEP - 1) / STEP);
     const int steps = total > warp ? (total - warp + CW - 1) / CW : 0;  // of this warp
     int used = 0;  // buffers filled so far: buffer used % STAGES, parity used / STAGES
     for (int s0 = 0; s0 < steps; s0 += SUPER) {
         // lane i: pages and scales of step s0 + i (two pages where they have 16 tokens)
         const int now = min(SUPER, steps - s0);
-        int page[2] = {-1, -1};
+        int tile[2] = {-1, -1};  // page * heads + head
         float ks[2] = {0.0f, 0.0f}, vs[2] = {0.0f, 0.0f};
         if (lane < now) {
             const int t = t_begin + ((s0 + lane) * CW + warp) * STEP;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if (t + 16 * h >= t_end) break;
-                const int p = c.table[(int64_t)b * c.max_pages + (t + 16 * h) / P];
+                const int p = c.table[(int64_t)b * c.max_pages + ((t + 16 * h) >> log_p)];
                 if ((unsigned)p < (unsigned)c.n_pages) {
-                    page[h] = p;
+                    tile[h] = p * c.n_kv + kvh;
                     ks[h] = c.k_scale[(int64_t)p * c.n_kv + kvh];
                     vs[h] = c.v_scale[(int64_t)p * c.n_kv + kvh];
                 } else {
@@ -271,7 +301,7 @@ __global__ void __launch_bounds__(CW * 32) cache_attn_kernel(const __grid_consta
         vs[1] = v_most > 0.0f ? vs[1] / v_most * P_UP : 0.0f;
 
         auto fetch = [&](int i) {
-            const int p0 = __shfl_sync(0xffffffffu, page[0], i), p1 = __shfl_sync(0xffffffffu, page[1], i);
+            const int p0 = __shfl_sync(0xffffffffu, tile[0], i), p1 = __shfl_sync(0xffffffffu, tile[1], i);
             const int at = (used + i) % STAGES;
             if (lane == 0) {
                 const int t = t_begin + ((s0 + i) * CW + warp) * STEP;
@@ -283,17 +313,17 @@ __global__ void __launch_bounds__(CW * 32) cache_attn_kernel(const __grid_consta
                     if (live) mbar_arrive_expect_tx(bar, live * C::TILE);
                     else mbar_arrive(bar);
                     if (p0 >= 0) {
-                        tma_load_3d(k, &tm_k, bar, 0, 0, p0 * c.n_kv + kvh);
-                        tma_load_3d(v, &tm_v, bar, 0, 0, p0 * c.n_kv + kvh);
+                        tma_load_3d(k, &tm_k, bar, 0, 0, p0);
+                        tma_load_3d(v, &tm_v, bar, 0, 0, p0);
                     }
                     if (p1 >= 0) {
-                        tma_load_3d(k + C::TILE / 2, &tm_k, bar, 0, 0, p1 * c.n_kv + kvh);
-                        tma_load_3d(v + C::TILE / 2, &tm_v, bar, 0, 0, p1 * c.n_kv + kvh);
+                        tma_load_3d(k + C::TILE / 2, &tm_k, bar, 0, 0, p1);
+                        tma_load_3d(v + C::TILE / 2, &tm_v, bar, 0, 0, p1);
                     }
                 } else if (p0 >= 0) {
                     mbar_arrive_expect_tx(bar, 2 * C::TILE);
-                    tma_load_3d(k, &tm_k, bar, 0, t % P, p0 * c.n_kv + kvh);
-                    tma_load_3d(v, &tm_v, bar, 0, t % P, p0 * c.n_kv + kvh);
+                    tma_load_3d(k, &tm_k, bar, 0, t & (P - 1), p0);
+                    tma_load_3d(v, &tm_v, bar, 0, t & (P - 1), p0);
                 } else {
                     mbar_arrive(bar);
                 }
@@ -310,89 +340,96 @@ __global__ void __launch_bounds__(CW * 32) cache_attn_kernel(const __grid_consta
                     mbar_wait_bounded(&bars[warp][(used + j) % STAGES], ((used + j) / STAGES) & 1, nullptr, sp.timeout_ns);
                 break;
             }
-            const uint8_t* k = mine + at * 2 * C::TILE;
-            const uint8_t* v = k + C::TILE;
+            const uint8_t* buf = mine + at * 2 * C::TILE;
+            const uint8_t *const k0 = buf + k_at[0], *const k1 = buf + k_at[1], *const v0 = buf + v_at[0], *const v1 = buf + v_at[1];
             const int t0 = t_begin + ((s0 + i) * CW + warp) * STEP;
 
-            float x[2][2][4];  // [16 tokens][8 tokens][2 tokens of query g, 2 of query g + 8]
+            float x[2][R][4];  // [16 tokens][queries 8 r ..][token g: queries 2c, 2c + 1; token g + 8: the same]
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < 2; ++u) {
+                uint32_t w[2][KS];  // this lane's codes of tokens g, g + 8
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const int row = 16 * u + 8 * j + g;
-                    uint32_t w[HD / 16];
+                    *reinterpret_cast<uint4*>(&w[j][0]) = *reinterpret_cast<const uint4*>(k0 + (16 * u + 8 * j) * HD);
+                    if constexpr (HD == 128) *reinterpret_cast<uint4*>(&w[j][4]) = *reinterpret_cast<const uint4*>(k1 + (16 * u + 8 * j) * HD);
+                }
 #pragma unroll
-                    for (int h = 0; h < HD / 64; ++h) {
-                        const int ch = HD == 128 ? (2 * cc + h) ^ (row & 7) : cc ^ ((row >> 1) & 3);
-                        *reinterpret_cast<uint4*>(&w[4 * h]) = *reinterpret_cast<const uint4*>(k + row * HD + ch * 16);
-                    }
+                for (int s = 0; s < KS; ++s) {
+                    const uint32_t y0 = w[0][s] ^ 0x80808080u, y1 = w[1][s] ^ 0x80808080u;
+                    const uint32_t a0 = codes_f16<0, 1>(y0), a1 = codes_f16<0, 1>(y1), a2 = codes_f16<2, 3>(y0), a3 = codes_f16<2, 3>(y1);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[u][j][e] = 0.0f;
-#pragma unroll
-                    for (int s = 0; s < KS; ++s) {
-                        w[s] ^= 0x80808080u;
-                        const uint32_t b0 = codes_f16<0, 1>(w[s]), b1 = codes_f16<2, 3>(w[s]);
+                    for (int r = 0; r < R; ++r)
 #pragma unroll
                         for (int y = 0; y < TERMS; ++y)
-                            mma_f16(x[u][j], qf[y][s][0][0], R == 2 ? qf[y][s][R - 1][0] : 0u, qf[y][s][0][1],
-                                    R == 2 ? qf[y][s][R - 1][1] : 0u, b0, b1);
-                    }
+                            if (s == 0 && y == 0) mma_f16_first(x[u][r], a0, a1, a2, a3, qf[y][s][r][0], qf[y][s][r][1]);
+                            else mma_f16(x[u][r], a0, a1, a2, a3, qf[y][s][r][0], qf[y][s][r][1]);
                 }
+            }
 
             // scores in units of log2, masked; the maxima that the exponentials refer to
-            const int p0 = __shfl_sync(0xffffffffu, page[0], i), p1 = __shfl_sync(0xffffffffu, page[1], i);
+            const int p0 = __shfl_sync(0xffffffffu, tile[0], i), p1 = __shfl_sync(0xffffffffu, tile[1], i);
             const float ks0 = __shfl_sync(0xffffffffu, ks[0], i), ks1 = __shfl_sync(0xffffffffu, ks[1], i);
             const float vs0 = __shfl_sync(0xffffffffu, vs[0], i), vs1 = __shfl_sync(0xffffffffu, vs[1], i);
             const bool whole = t0 + STEP <= t_end && p0 >= 0 && p1 >= 0;
-            float mx[R];
             bool grown = false;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const float f0 = ks0 * qs[r], f1 = ks1 * qs[r];
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
+                    for (int e = 0; e < 4; ++e) x[u][r][e] *= (u ? ks1 : ks0) * qs[r][e & 1];
+            }
+            if (!whole) {
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) x[u][j][2 * r + e] *= u ? f1 : f0;
-                if (!whole) {
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if ((u ? p1 : p0) < 0 || t0 + 16 * u + 8 * h + g >= t_end) {
+#pragma unroll
+                            for (int r = 0; r < R; ++r) x[u][r][2 * h] = x[u][r][2 * h + 1] = -INFINITY;
+                        }
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    grown |= max3(fmaxf(x[0][r][e], x[0][r][2 + e]), x[1][r][e], x[1][r][2 + e]) - m[r][e] > GROW;
+            }
+            if (a.accumulate) {
+                float* to = scores + (int64_t)t0 * sp.ws.group;
+#pragma unroll
+                for (int r = 0; r < R; ++r)
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                if ((u ? p1 : p0) < 0 || t0 + 16 * u + 8 * j + 2 * cc + e >= t_end) x[u][j][2 * r + e] = -INFINITY;
-                }
-                mx[r] = max3(fmaxf(x[0][0][2 * r], x[0][0][2 * r + 1]), x[0][1][2 * r], x[0][1][2 * r + 1]);
-                mx[r] = max3(max3(mx[r], x[1][0][2 * r], x[1][0][2 * r + 1]), x[1][1][2 * r], x[1][1][2 * r + 1]);
-                mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-                mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-                grown |= mx[r] - m[r] > GROW;
-                if (a.accumulate && g + 8 * r < n_q) {
-                    float* to = scores[r] + t0;
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            if (whole || t0 + 16 * u + 8 * j + 2 * cc < t_end)
-                                *reinterpret_cast<float2*>(to + 16 * u + 8 * j) = make_float2(x[u][j][2 * r], x[u][j][2 * r + 1]);
-                }
+                        for (int h = 0; h < 2; ++h) {
+                            if (!whole && t0 + 16 * u + 8 * h + g >= t_end) continue;
+                            float* y = to + (16 * u + 8 * h) * sp.ws.group + 8 * r;
+                            const int q = 8 * r + 2 * cc;  // an even group keeps pairs aligned
+                            if (q + 1 < n_q && (sp.ws.group & 1) == 0) {
+                                *reinterpret_cast<float2*>(y) = make_float2(x[u][r][2 * h], x[u][r][2 * h + 1]);
+                            } else {
+                                if (q < n_q) y[0] = x[u][r][2 * h];
+                                if (q + 1 < n_q) y[1] = x[u][r][2 * h + 1];
+                            }
+                        }
             }
             if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    float alpha = 1.0f;
-                    if (mx[r] - m[r] > GROW) {
-                        alpha = m[r] == -INFINITY ? 0.0f : exp2_fast(m[r] - mx[r]);
-                        m[r] = mx[r];
-                    }
-                    l[r] *= alpha;
-                    const float f0 = __shfl_sync(0xffffffffu, alpha, 8 * cc), f1 = __shfl_sync(0xffffffffu, alpha, 8 * cc + 4);
+                for (int r = 0; r < R; ++r)
 #pragma unroll
-                    for (int y = 0; y < ND / 2; ++y)
-                        acc[r][y][0] *= f0, acc[r][y][1] *= f1, acc[r][y][2] *= f0, acc[r][y][3] *= f1;
-                }
+                    for (int e = 0; e < 2; ++e) {
+                        float mx = max3(fmaxf(x[0][r][e], x[0][r][2 + e]), x[1][r][e], x[1][r][2 + e]);
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                        if (mx - m[r][e] > GROW) {
+                            const float alpha = m[r][e] == -INFINITY ? 0.0f : exp2_fast(m[r][e] - mx);
+                            m[r][e] = mx;
+                            l[r][e] *= alpha;
+#pragma unroll
+                            for (int y = 0; y < ND / 2; ++y) acc[r][y][e] *= alpha, acc[r][y][2 + e] *= alpha;
+                        }
+                    }
             }
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -400,26 +437,22 @@ __global__ void __launch_bounds__(CW * 32) cache_attn_kernel(const __grid_consta
                 uint32_t pf[TERMS][R][2];
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    const float ms = m[r] == -INFINITY ? 0.0f : m[r];
+                    const float ms0 = m[r][0] == -INFINITY ? 0.0f : m[r][0], ms1 = m[r][1] == -INFINITY ? 0.0f : m[r][1];
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float e0 = exp2_fast(x[u][j][2 * r] - ms), e1 = exp2_fast(x[u][j][2 * r + 1] - ms);
-                        l[r] += e0 + e1;
-                        pf[0][r][j] = pair_f16(e0 * vf, e1 * vf);
-                        if constexpr (TERMS == 2) pf[1][r][j] = rest_f16(e0 * vf, e1 * vf, pf[0][r][j]);
+                    for (int h = 0; h < 2; ++h) {
+                        const float e0 = exp2_fast(x[u][r][2 * h] - ms0), e1 = exp2_fast(x[u][r][2 * h + 1] - ms1);
+                        l[r][0] += e0, l[r][1] += e1;
+                        const uint32_t hi = pair_f16(e0 * vf, e1 * vf);
+                        pf[0][r][h] = transposed(hi);
+                        if constexpr (TERMS == 2) pf[1][r][h] = transposed(rest_f16(e0 * vf, e1 * vf, hi));
                     }
                 }
                 uint32_t w[4][ND / 4];  // [tokens 2c, 2c + 1, 2c + 8, 2c + 9][this lane's d / 8 codes]
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
-                    const int row = 16 * u + 2 * cc + (h & 1) + 8 * (h >> 1);
-                    if constexpr (HD == 128) {
-                        *reinterpret_cast<uint4*>(&w[h][0]) =
-                            *reinterpret_cast<const uint4*>(v + row * HD + ((g ^ (row & 7)) << 4));
-                    } else {
-                        *reinterpret_cast<uint2*>(&w[h][0]) = *reinterpret_cast<const uint2*>(
-                            v + row * HD + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + 8 * (g & 1));
-                    }
+                    const uint8_t* from = (h & 1 ? v1 : v0) + (16 * u + 8 * (h >> 1)) * HD;
+                    if constexpr (HD == 128) *reinterpret_cast<uint4*>(&w[h][0]) = *reinterpret_cast<const uint4*>(from);
+                    else *reinterpret_cast<uint2*>(&w[h][0]) = *reinterpret_cast<const uint2*>(from);
 #pragma unroll
                     for (int y = 0; y < ND / 4; ++y) w[h][y] ^= 0x80808080u;
                 }
@@ -448,11 +481,13 @@ __global__ void __launch_bounds__(CW * 32) cache_attn_kernel(const __grid_consta
 
     // ---- the block's warps joined: o[w][query][d] in the ring, relative to the common maximum
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-        if (cc == 0) sh_m[warp][g + 8 * r] = m[r], sh_l[warp][g + 8 * r] = l[r];
-    }
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) l[r][e] += __shfl_xor_sync(0xffffffffu, l[r][e], o);
+            if (g == 0) sh_m[warp][8 * r + 2 * cc + e] = m[r][e], sh_l[warp][8 * r + 2 * cc + e] = l[r][e];
+        }
     if (!__syncthreads_and(ok)) return;
     constexpr int LD = HD + 4;
     float* out = reinterpret_cast<float*>(ring);
@@ -466,7 +501,7 @@ __global__ void __launch_bounds__(CW * 32) cache_attn_kernel(const __grid_consta
 #pragma unroll
             for (int w = 1; w < CW; ++w) top = fmaxf(top, sh_m[w][q]);
             const float mw = sh_m[warp][q];
-            const float f = mw == -INFINITY ? 0.0f : exp2f(mw - top) * (v_most * (1.0f / P_UP));
+            const float f = mw == -INFINITY ? 0.0f : exp2_fast(mw - top) * (v_most * (1.0f / P_UP));
             float* to = out + (warp * QT + q) * LD + ND * g;
 #pragma unroll
             for (int y = 0; y < ND / 4; ++y)
@@ -474,124 +509,133 @@ __global__ void __launch_bounds__(CW * 32) cache_attn_kernel(const __grid_consta
                                                                      acc[r][2 * y + 1][e] * f, acc[r][2 * y + 1][2 + e] * f);
         }
     __syncthreads();
-    for (int i = tid; i < n_q * HD; i += CW * 32) {
-        const int q = i / HD, d = i % HD;
-        float top = sh_m[0][q], sum = 0.0f, o = 0.0f;
+    for (int i = tid; i < n_q * (HD / 4); i += CW * 32) {
+        const int q = i / (HD / 4), d = i % (HD / 4) * 4;
+        float top = sh_m[0][q], sum = 0.0f;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 1; w < CW; ++w) top = fmaxf(top, sh_m[w][q]);
 #pragma unroll
         for (int w = 0; w < CW; ++w) {
             const float mw = sh_m[w][q];
-            sum += mw == -INFINITY ? 0.0f : sh_l[w][q] * exp2f(mw - top);
-            o += out[(w * QT + q) * LD + d];
+            sum += mw == -INFINITY ? 0.0f : sh_l[w][q] * exp2_fast(mw - top);
+            const float4 y = *reinterpret_cast<const float4*>(out + (w * QT + q) * LD + d);
+            o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
         }
         const int64_t row = (int64_t)b * a.n_heads + head0 + q;
         if (d == 0) sp.ws.ml[row * sp.ws.splits + split] = make_float2(top, sum);
         if (sp.ws.splits > 1) {
-            sp.ws.part[(row * sp.ws.splits + split) * HD + d] = o;
+            *reinterpret_cast<float4*>(sp.ws.part + (row * sp.ws.splits + split) * HD + d) = o;
         } else {
-            static_cast<T*>(a.o)[b * a.ld_o + (int64_t)(head0 + q) * HD + d] = from_f<T>(sum == 0.0f ? 0.0f : o / sum);
-            if (d == 0) {
-                if (a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : top * LN2 + logf(sum);
-            }
+            T* to = static_cast<T*>(a.o) + b * a.ld_o + (int64_t)(head0 + q) * HD + d;
+            const float y[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) to[e] = from_f<T>(sum == 0.0f ? 0.0f : y[e] / sum);
+            if (d == 0 && a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : top * LN2 + logf(sum);
         }
     }
 }
 
 // What remains when the splits are done, per (sequence, kv head).  With more than one split the first
-// blocks join the outputs of one query head each; the others add the probabilities of 1024 tokens to
-// their weights,
+// blocks join the outputs of `per_block` query heads each, 8 / per_block warps to a head; the others
+// add the probabilities of FIN_TOKENS tokens to their weights,
 //     weight(t) += sum over the heads of the group of exp2(score - lse).
-constexpr int FIN = 256;
+constexpr int FIN = 256, FIN_TOKENS = 2048;
+struct FinishArgs {
+    CacheAttnArgs a;
+    AttnWs ws;
+    int joins, per_block;
+};
+// Maximum and sum (relative to it) of a query head over its splits; weights of the splits to f.
+__device__ __forceinline__ float2 join_sums(const AttnWs& ws, int64_t row, int live, float* f) {
+    const int lane = threadIdx.x & 31;
+    float top = -INFINITY, l = 0.0f;
+    for (int s = lane; s < live; s += 32) top = fmaxf(top, ws.ml[row * ws.splits + s].x);
+    top = warp_max(top);
+    for (int s = lane; s < live; s += 32) {
+        const float2 ml = ws.ml[row * ws.splits + s];
+        const float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - top);
+        if (f) f[s] = w;
+        l += ml.x == -INFINITY ? 0.0f : ml.y * w;
+    }
+    return make_float2(top, warp_sum(l));
+}
 template <typename T, int HD>
-__global__ void __launch_bounds__(FIN) cache_finish_kernel(const CacheAttnArgs a, const AttnWs ws) {
+__global__ void __launch_bounds__(FIN) cache_finish_kernel(const FinishArgs fa) {
+    const CacheAttnArgs& a = fa.a;
+    const AttnWs& ws = fa.ws;
     const CacheArgs& c = a.c;
     wait_for_earlier_grid();
     if (stopped(c.status)) return;
-    const int b = blockIdx.z, kvh = blockIdx.y, group = a.n_heads / c.n_kv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int b = blockIdx.z, kvh = blockIdx.y, group = ws.group, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     bool bad;
     const int n = cached_len(c, b, bad);
     const int live = max(1, (n + ws.chunk - 1) / ws.chunk);
     const int64_t row0 = (int64_t)b * a.n_heads + kvh * group;
-    const int joins = ws.splits > 1 ? group : 0;
-    if ((int)blockIdx.x < joins) {
-        __shared__ float f[MAX_SPLITS], sums[FIN / 32][HD], total;
-        const int64_t row = row0 + blockIdx.x;
-        if (warp == 0) {
-            float top = -INFINITY, l = 0.0f;
-            for (int s = lane; s < live; s += 32) top = fmaxf(top, ws.ml[row * ws.splits + s].x);
-            top = warp_max(top);
-            for (int s = lane; s < live; s += 32) {
-                const float2 ml = ws.ml[row * ws.splits + s];
-                f[s] = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - top);
-                l += ml.x == -INFINITY ? 0.0f : ml.y * f[s];
-            }
-            l = warp_sum(l);
-            if (lane == 0) {
-                total = l;
-                if (a.lse) a.lse[row] = l == 0.0f ? -INFINITY : top * LN2 + logf(l);
-            }
-        }
-        __syncthreads();
-        const float* part = ws.part + row * ws.splits * HD + lane * (HD / 32);
-        float o[HD / 32] = {};
+    if ((int)blockIdx.x < fa.joins) {
+        constexpr int E = HD / 32;
+        __shared__ float f[FIN / 32][MAX_SPLITS], sums[FIN / 32][HD];
+        const int warps = FIN / 32 / fa.per_block, sub = warp % warps;
+        const int h = blockIdx.x * fa.per_block + warp / warps;
+        const int64_t row = row0 + h;
+        float2 ml = make_float2(0.0f, 0.0f);
+        if (h < group) {
+            ml = join_sums(ws, row, live, f[warp]);
+            __syncwarp();
+            const float* part = ws.part + row * ws.splits * HD + lane * E;
+            float o[E] = {};
 #pragma unroll 4
-        for (int s = warp; s < live; s += FIN / 32) {
-            const float w = f[s];
+            for (int s = sub; s < live; s += warps) {
+                const float w = f[warp][s];
 #pragma unroll
-            for (int e = 0; e < HD / 32; ++e) o[e] += part[(int64_t)s * HD + e] * w;
+                for (int e = 0; e < E; ++e) o[e] += part[(int64_t)s * HD + e] * w;
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) sums[warp][lane * E + e] = o[e];
         }
-#pragma unroll
-        for (int e = 0; e < HD / 32; ++e) sums[warp][lane * (HD / 32) + e] = o[e];
         __syncthreads();
-        if (tid < HD) {
-            float y = 0.0f;
-#pragma unroll
-            for (int w = 0; w < FIN / 32; ++w) y += sums[w][tid];
-            static_cast<T*>(a.o)[b * a.ld_o + (int64_t)(kvh * group + blockIdx.x) * HD + tid] = from_f<T>(total == 0.0f ? 0.0f : y / total);
+        if (h < group && sub == 0) {
+            T* to = static_cast<T*>(a.o) + b * a.ld_o + (int64_t)(kvh * group + h) * HD;
+            for (int d = lane; d < HD; d += 32) {
+                float y = 0.0f;
+                for (int w = 0; w < warps; ++w) y += sums[warp + w][d];
+                to[d] = from_f<T>(ml.y == 0.0f ? 0.0f : y / ml.y);
+            }
+            if (lane == 0 && a.lse) a.lse[row] = ml.y == 0.0f ? -INFINITY : ml.x * LN2 + logf(ml.y);
         }
         return;
     }
-    const int t0 = ((int)blockIdx.x - joins) * 4 * FIN;
+    const int t0 = ((int)blockIdx.x - fa.joins) * FIN_TOKENS;
     if (t0 >= n) return;
-    const int t = t0 + 4 * tid;
-    int page = -1;
-    if (t < n) page = c.table[(int64_t)b * c.max_pages + t / c.page_len];  // 4 tokens never cross a page
-    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    __shared__ float lse2[64];
-    for (int h0 = 0; h0 < group; h0 += 64) {
-        const int some = min(64, group - h0);
-        __syncthreads();
-        for (int h = warp; h < some; h += FIN / 32) {  // the sums of the heads over the splits
-            const int64_t row = row0 + h0 + h;
-            float top = -INFINITY, l = 0.0f;
-            for (int s = lane; s < live; s += 32) top = fmaxf(top, ws.ml[row * ws.splits + s].x);
-            top = warp_max(top);
-            for (int s = lane; s < live; s += 32) {
-                const float2 ml = ws.ml[row * ws.splits + s];
-                l += ml.x == -INFINITY ? 0.0f : ml.y * exp2f(ml.x - top);
-            }
-            l = warp_sum(l);
-            if (lane == 0) lse2[h] = top + log2f(l);
+    const int end = min(n, t0 + FIN_TOKENS), log_p = __ffs(c.page_len) - 1;
+    __shared__ float lse2[32];
+    for (int h0 = 0; h0 < group; h0 += 32) {
+        const int some = min(32, group - h0);
+        if (h0 > 0) __syncthreads();
+        for (int h = warp; h < some; h += FIN / 32) {
+            const float2 ml = join_sums(ws, row0 + h0 + h, live, nullptr);
+            if (lane == 0) lse2[h] = ml.x + log2f(ml.y);
         }
         __syncthreads();
-        if ((unsigned)page < (unsigned)c.n_pages) {
-            const float* x = ws.scores + (row0 + h0) * ws.stride + t;
-#pragma unroll 8
-            for (int h = 0; h < some; ++h) {
-                const float4 y = *reinterpret_cast<const float4*>(x + (int64_t)h * ws.stride);
-                const float z = lse2[h];
-                sum.x += exp2f(y.x - z), sum.y += exp2f(y.y - z), sum.z += exp2f(y.z - z), sum.w += exp2f(y.w - z);
+        const float* x = ws.scores + ((int64_t)b * c.n_kv + kvh) * ws.stride * group + h0;
+#pragma unroll 4
+        for (int t = t0 + tid; t < end; t += FIN) {
+            const int page = c.table[(int64_t)b * c.max_pages + (t >> log_p)];
+            const float* y = x + (int64_t)t * group;
+            float sum = 0.0f;
+            if (group % 4 == 0) {  // 16-byte aligned: h0 and the group are multiples of 4
+                for (int h = 0; h < some; h += 4) {
+                    const float4 z = *reinterpret_cast<const float4*>(y + h);
+                    sum += exp2f(z.x - lse2[h]) + exp2f(z.y - lse2[h + 1]) + exp2f(z.z - lse2[h + 2]) + exp2f(z.w - lse2[h + 3]);
+                }
+            } else {
+                for (int h = 0; h < some; ++h) sum += exp2f(y[h] - lse2[h]);
             }
+            // a page of one sequence has one writer per call; sequences that share a page add in any order
+            if ((unsigned)page < (unsigned)c.n_pages)
+                atomicAdd(c.weight + ((int64_t)page * c.n_kv + kvh) * c.page_len + (t & (c.page_len - 1)), sum);
         }
     }
-    if ((unsigned)page >= (unsigned)c.n_pages) return;
-    // a page of one sequence has one writer per call; sequences that share a page add in any order
-    float* w = c.weight + ((int64_t)page * c.n_kv + kvh) * c.page_len + t % c.page_len;
-    atomicAdd(w, sum.x);
-    if (t + 1 < n) atomicAdd(w + 1, sum.y);
-    if (t + 2 < n) atomicAdd(w + 2, sum.z);
-    if (t + 3 < n) atomicAdd(w + 3, sum.w);
 }
 
 size_t cache_attention_ws_bytes(int batch, int max_len, int n_heads, int n_kv, int head_dim, bool accumulate) {
@@ -639,9 +683,14 @@ static cudaError_t cache_attn(const CacheAttnArgs& a, cudaStream_t st) {
     const dim3 grid(sp.ws.splits, a.c.n_kv * sp.q_tiles, a.c.batch);
     cache_attn_kernel<T, HD, QT><<<grid, CW * 32, DCfg<HD>::SMEM, st>>>(tm_k, tm_v, a, sp);
     e = cudaGetLastError();
-    const int finish = (sp.ws.splits > 1 ? a.n_heads / a.c.n_kv : 0) + (a.accumulate ? cdiv(a.c.max_len, 4 * FIN) : 0);
-    if (e == cudaSuccess && finish > 0)
-        e = launch_early(cache_finish_kernel<T, HD>, dim3(finish, a.c.n_kv, a.c.batch), FIN, st, a, sp.ws);
+    FinishArgs f;
+    f.a = a, f.ws = sp.ws;
+    // few heads: all warps of a block to each; many: a warp each, which has fewer blocks to start
+    f.per_block = (int64_t)a.c.batch * a.n_heads <= 4 * 148 ? 1 : FIN / 32;
+    f.joins = sp.ws.splits > 1 ? cdiv(sp.ws.group, f.per_block) : 0;
+    const int blocks = f.joins + (a.accumulate ? cdiv(a.c.max_len, FIN_TOKENS) : 0);
+    if (e == cudaSuccess && blocks > 0)
+        e = launch_early(cache_finish_kernel<T, HD>, dim3(blocks, a.c.n_kv, a.c.batch), FIN, st, f);
     return e;
 }
 
