@@ -287,44 +287,74 @@ def energon_kernel_binary_version() -> int:
 # ----------------------------------------------------------------------------- serving
 
 
-def _rows(x, rows: int, ld: int, width: int, dtype: int, what: str) -> int:
+# These calls are short enough that marshalling counts: each argument is looked at once, by the
+# cheapest question that answers it.
+
+
+def _device() -> int:
+    """The device that the library will launch on; -1 where there is none."""
+    try:
+        return torch._C._cuda_getDevice()
+    except Exception:  # no CUDA build or no device: every tensor argument is then refused
+        return -1
+
+
+def _raw_stream(s, device: int) -> int:
+    if s is None:
+        return torch._C._cuda_getCurrentRawStream(device) if device >= 0 else 0
+    return s if isinstance(s, int) else s.cuda_stream
+
+
+def _misplaced(x, device: int, what: str):
+    if not x.is_cuda:
+        return ValueError(f"{what}: tensor must live on a CUDA device")
+    return ValueError(f"{what}: a tensor on {x.device}, the current device is cuda:{device}")
+
+
+def _rows(x, rows: int, ld: int, width: int, dtype: int, what: str, device: int) -> int:
     """Device pointer of `rows` rows of `width` elements, `ld` elements apart.  A tensor may be a view
     into wider rows (its last dimensions dense, its first of stride ld); it must be of `dtype` and
     its memory must reach to the end of the last row."""
     if not isinstance(x, torch.Tensor):
         return _dev(x, what)
-    if not x.is_cuda:
-        raise ValueError(f"{what}: tensor must live on a CUDA device")
+    if x.get_device() != device or device < 0:
+        raise _misplaced(x, device, what)
     if x.dtype is not TORCH_DTYPE.get(dtype):
         raise ValueError(f"{what}: a {x.dtype} tensor, the call says dtype {dtype}")
     if rows > 0 and width > 0:
-        end = (rows - 1) * ld + width
         if x.is_contiguous():
             have = x.numel()
         elif x.dim() >= 2 and x[0].is_contiguous() and x.stride(0) == ld:
             have = (x.shape[0] - 1) * ld + x[0].numel()
         else:
             raise ValueError(f"{what}: rows must be dense and {ld} elements apart")
-        if have < end:
-            raise ValueError(f"{what}: {have} elements, the call needs {end}")
+        if have < (rows - 1) * ld + width:
+            raise ValueError(f"{what}: {have} elements, the call needs {(rows - 1) * ld + width}")
     return x.data_ptr()
 
 
-def _same_device(*tensors) -> None:
-    """The library launches on the current device: every tensor has to live there."""
-    here = torch.cuda.current_device() if torch.cuda.is_available() else None
-    for x in tensors:
-        if isinstance(x, torch.Tensor) and x.is_cuda and x.device.index != here:
-            raise ValueError(f"a tensor on {x.device}, the current device is cuda:{here}")
+def _arg(x, elems: int, dtype, what: str, device: int) -> int:
+    """Device pointer of a dense tensor of `dtype` with at least `elems` elements."""
+    if x is None:
+        return 0
+    if not isinstance(x, torch.Tensor):
+        return _dev(x, what)
+    if x.get_device() != device or device < 0:
+        raise _misplaced(x, device, what)
+    if dtype is not None and x.dtype is not dtype:
+        raise ValueError(f"{what}: a {x.dtype} tensor, expected {dtype}")
+    if not x.is_contiguous():
+        raise ValueError(f"{what}: tensor must be contiguous")
+    if x.numel() < elems:
+        raise ValueError(f"{what}: {x.numel()} elements, the call needs {elems}")
+    return x.data_ptr()
 
 
-def _arg(x, nbytes: int, dtype, what: str) -> int:
-    """Device pointer of a dense tensor of `dtype` with at least `nbytes` bytes."""
-    if isinstance(x, torch.Tensor):
-        if x.dtype is not dtype:
-            raise ValueError(f"{what}: a {x.dtype} tensor, expected {dtype}")
-        _need(x, nbytes, what)
-    return _dev(x, what)
+def _workspace(x, nbytes: int, device: int) -> int:
+    if isinstance(x, torch.Tensor) and x.dtype is torch.uint8:
+        return _arg(x, nbytes, None, "workspace", device)
+    _need(x, nbytes, "workspace")
+    return _arg(x, 0, None, "workspace", device)
 
 
 def make_kv_cache(k_codes, v_codes, k_scale, v_scale, weight=None) -> energon_kv_cache:
@@ -333,49 +363,47 @@ def make_kv_cache(k_codes, v_codes, k_scale, v_scale, weight=None) -> energon_kv
     if k_codes.dim() != 4 or k_codes.shape != v_codes.shape:
         raise ValueError("k_codes and v_codes: expected two [n_pages, n_kv_heads, page_len, head_dim] tensors")
     n, kv, p, d = k_codes.shape
-    _same_device(k_codes, v_codes, k_scale, v_scale, weight)
-    return energon_kv_cache(_arg(k_codes, n * kv * p * d, torch.int8, "k_codes"),
-                            _arg(v_codes, n * kv * p * d, torch.int8, "v_codes"),
-                            _arg(k_scale, 4 * n * kv, torch.float32, "k_scale"),
-                            _arg(v_scale, 4 * n * kv, torch.float32, "v_scale"),
-                            _arg(weight, 4 * n * kv * p, torch.float32, "weight"), n, kv, p, d)
+    dev, f32 = _device(), torch.float32
+    return energon_kv_cache(_arg(k_codes, 0, torch.int8, "k_codes", dev), _arg(v_codes, 0, torch.int8, "v_codes", dev),
+                            _arg(k_scale, n * kv, f32, "k_scale", dev), _arg(v_scale, n * kv, f32, "v_scale", dev),
+                            _arg(weight, n * kv * p, f32, "weight", dev), n, kv, p, d)
 
 
 def energon_prompt_attention(q, ld_q, k, ld_k, v, ld_v, cu_seqlens, batch, rows, n_heads, n_kv_heads, head_dim, dtype,
                              scale, o, ld_o, lse=None, d_status=None, stream=None) -> None:
-    _same_device(q, k, v, cu_seqlens, o, lse, d_status)
+    dev = _device()
     wq, wk = n_heads * head_dim, n_kv_heads * head_dim
     _check(load().energon_prompt_attention(
-        _rows(q, rows, ld_q, wq, dtype, "q"), ld_q, _rows(k, rows, ld_k, wk, dtype, "k"), ld_k,
-        _rows(v, rows, ld_v, wk, dtype, "v"), ld_v, _arg(cu_seqlens, 4 * (batch + 1), torch.int32, "cu_seqlens"), batch,
-        rows, n_heads, n_kv_heads, head_dim, dtype, scale, _rows(o, rows, ld_o, wq, dtype, "o"), ld_o,
-        _arg(lse, 4 * n_heads * rows, torch.float32, "lse"), _arg(d_status, 4, torch.int32, "d_status"),
-        _stream(stream)), "energon_prompt_attention")
+        _rows(q, rows, ld_q, wq, dtype, "q", dev), ld_q, _rows(k, rows, ld_k, wk, dtype, "k", dev), ld_k,
+        _rows(v, rows, ld_v, wk, dtype, "v", dev), ld_v, _arg(cu_seqlens, batch + 1, torch.int32, "cu_seqlens", dev), batch,
+        rows, n_heads, n_kv_heads, head_dim, dtype, scale, _rows(o, rows, ld_o, wq, dtype, "o", dev), ld_o,
+        _arg(lse, n_heads * rows, torch.float32, "lse", dev), _arg(d_status, 1, torch.int32, "d_status", dev),
+        _raw_stream(stream, dev)), "energon_prompt_attention")
 
 
 def energon_prompt_key_weights(q, ld_q, k, ld_k, lse, cu_seqlens, batch, rows, n_heads, n_kv_heads, head_dim, dtype,
                                scale, window, weights, d_status=None, stream=None) -> None:
-    _same_device(q, k, lse, cu_seqlens, weights, d_status)
+    dev = _device()
     _check(load().energon_prompt_key_weights(
-        _rows(q, rows, ld_q, n_heads * head_dim, dtype, "q"), ld_q,
-        _rows(k, rows, ld_k, n_kv_heads * head_dim, dtype, "k"), ld_k,
-        _arg(lse, 4 * n_heads * rows, torch.float32, "lse"),
-        _arg(cu_seqlens, 4 * (batch + 1), torch.int32, "cu_seqlens"), batch, rows, n_heads, n_kv_heads, head_dim, dtype,
-        scale, min(int(window), 0x7fffffff), _arg(weights, 4 * n_kv_heads * rows, torch.float32, "weights"),
-        _arg(d_status, 4, torch.int32, "d_status"), _stream(stream)), "energon_prompt_key_weights")
+        _rows(q, rows, ld_q, n_heads * head_dim, dtype, "q", dev), ld_q,
+        _rows(k, rows, ld_k, n_kv_heads * head_dim, dtype, "k", dev), ld_k,
+        _arg(lse, n_heads * rows, torch.float32, "lse", dev),
+        _arg(cu_seqlens, batch + 1, torch.int32, "cu_seqlens", dev), batch, rows, n_heads, n_kv_heads, head_dim, dtype,
+        scale, min(int(window), 0x7fffffff), _arg(weights, n_kv_heads * rows, torch.float32, "weights", dev),
+        _arg(d_status, 1, torch.int32, "d_status", dev), _raw_stream(stream, dev)), "energon_prompt_key_weights")
 
 
 def energon_kv_append(cache, page_table, max_pages, cache_lens, k, ld_k, v, ld_v, weights, cu_seqlens, batch, rows, dtype,
                       d_status=None, stream=None) -> None:
-    _same_device(page_table, cache_lens, k, v, weights, cu_seqlens, d_status)
+    dev = _device()
     width = cache.n_kv_heads * cache.head_dim
     _check(load().energon_kv_append(
-        ctypes.byref(cache), _arg(page_table, 4 * batch * max_pages, torch.int32, "page_table"), max_pages,
-        _arg(cache_lens, 4 * batch, torch.int32, "cache_lens"), _rows(k, rows, ld_k, width, dtype, "k"), ld_k,
-        _rows(v, rows, ld_v, width, dtype, "v"), ld_v,
-        _arg(weights, 4 * cache.n_kv_heads * rows, torch.float32, "weights"),
-        _arg(cu_seqlens, 4 * (batch + 1), torch.int32, "cu_seqlens"), batch, rows, dtype,
-        _arg(d_status, 4, torch.int32, "d_status"), _stream(stream)), "energon_kv_append")
+        ctypes.byref(cache), _arg(page_table, batch * max_pages, torch.int32, "page_table", dev), max_pages,
+        _arg(cache_lens, batch, torch.int32, "cache_lens", dev), _rows(k, rows, ld_k, width, dtype, "k", dev), ld_k,
+        _rows(v, rows, ld_v, width, dtype, "v", dev), ld_v,
+        _arg(weights, cache.n_kv_heads * rows, torch.float32, "weights", dev),
+        _arg(cu_seqlens, batch + 1, torch.int32, "cu_seqlens", dev), batch, rows, dtype,
+        _arg(d_status, 1, torch.int32, "d_status", dev), _raw_stream(stream, dev)), "energon_kv_append")
 
 
 def energon_cache_attention_workspace_bytes(cache, batch, max_len, n_heads, accumulate) -> int:
@@ -386,16 +414,15 @@ def energon_cache_attention_workspace_bytes(cache, batch, max_len, n_heads, accu
 def energon_cache_attention(cache, page_table, max_pages, cache_lens, batch, max_len, q, ld_q, n_heads, dtype, scale, o,
                             ld_o, lse=None, accumulate=0, d_status=None, workspace=None, ws_bytes=0,
                             stream=None) -> None:
-    _same_device(page_table, cache_lens, q, o, lse, d_status, workspace)
+    dev = _device()
     width = n_heads * cache.head_dim
-    _need(workspace, ws_bytes, "workspace")
     _check(load().energon_cache_attention(
-        ctypes.byref(cache), _arg(page_table, 4 * batch * max_pages, torch.int32, "page_table"), max_pages,
-        _arg(cache_lens, 4 * batch, torch.int32, "cache_lens"), batch, max_len,
-        _rows(q, batch, ld_q, width, dtype, "q"), ld_q, n_heads, dtype, scale,
-        _rows(o, batch, ld_o, width, dtype, "o"), ld_o, _arg(lse, 4 * batch * n_heads, torch.float32, "lse"),
-        int(accumulate), _arg(d_status, 4, torch.int32, "d_status"), _dev(workspace, "workspace"), ws_bytes,
-        _stream(stream)), "energon_cache_attention")
+        ctypes.byref(cache), _arg(page_table, batch * max_pages, torch.int32, "page_table", dev), max_pages,
+        _arg(cache_lens, batch, torch.int32, "cache_lens", dev), batch, max_len,
+        _rows(q, batch, ld_q, width, dtype, "q", dev), ld_q, n_heads, dtype, scale,
+        _rows(o, batch, ld_o, width, dtype, "o", dev), ld_o, _arg(lse, batch * n_heads, torch.float32, "lse", dev),
+        int(accumulate), _arg(d_status, 1, torch.int32, "d_status", dev), _workspace(workspace, ws_bytes, dev), ws_bytes,
+        _raw_stream(stream, dev)), "energon_cache_attention")
 
 
 def energon_cache_evict_workspace_bytes(cache, batch, budget) -> int:
@@ -404,14 +431,13 @@ def energon_cache_evict_workspace_bytes(cache, batch, budget) -> int:
 
 def energon_cache_evict(cache, page_table, max_pages, cache_lens, new_page_table, new_max_pages, new_lens, batch, max_len,
                         budget, recent, d_status=None, workspace=None, ws_bytes=0, stream=None) -> None:
-    _same_device(page_table, cache_lens, new_page_table, new_lens, d_status, workspace)
-    _need(workspace, ws_bytes, "workspace")
+    dev = _device()
     _check(load().energon_cache_evict(
-        ctypes.byref(cache), _arg(page_table, 4 * batch * max_pages, torch.int32, "page_table"), max_pages,
-        _arg(cache_lens, 4 * batch, torch.int32, "cache_lens"),
-        _arg(new_page_table, 4 * batch * new_max_pages, torch.int32, "new_page_table"), new_max_pages,
-        _arg(new_lens, 4 * batch, torch.int32, "new_lens"), batch, max_len, budget, recent,
-        _arg(d_status, 4, torch.int32, "d_status"), _dev(workspace, "workspace"), ws_bytes, _stream(stream)),
+        ctypes.byref(cache), _arg(page_table, batch * max_pages, torch.int32, "page_table", dev), max_pages,
+        _arg(cache_lens, batch, torch.int32, "cache_lens", dev),
+        _arg(new_page_table, batch * new_max_pages, torch.int32, "new_page_table", dev), new_max_pages,
+        _arg(new_lens, batch, torch.int32, "new_lens", dev), batch, max_len, budget, recent,
+        _arg(d_status, 1, torch.int32, "d_status", dev), _workspace(workspace, ws_bytes, dev), ws_bytes, _raw_stream(stream, dev)),
         "energon_cache_evict")
 
 

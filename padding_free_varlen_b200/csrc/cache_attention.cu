@@ -618,22 +618,34 @@ __global__ void __launch_bounds__(FIN) cache_finish_kernel(const FinishArgs fa) 
         }
         __syncthreads();
         const float* x = ws.scores + ((int64_t)b * c.n_kv + kvh) * ws.stride * group + h0;
-#pragma unroll 4
-        for (int t = t0 + tid; t < end; t += FIN) {
-            const int page = c.table[(int64_t)b * c.max_pages + (t >> log_p)];
-            const float* y = x + (int64_t)t * group;
-            float sum = 0.0f;
+        constexpr int K = 4;  // tokens of a thread at a time: their loads are on their way together
+        for (int t = t0 + tid; t < end; t += K * FIN) {
+            int page[K];
+            float sum[K] = {};
+#pragma unroll
+            for (int k = 0; k < K; ++k) page[k] = t + k * FIN < end ? c.table[(int64_t)b * c.max_pages + ((t + k * FIN) >> log_p)] : -1;
             if (group % 4 == 0) {  // 16-byte aligned: h0 and the group are multiples of 4
+#pragma unroll 2
                 for (int h = 0; h < some; h += 4) {
-                    const float4 z = *reinterpret_cast<const float4*>(y + h);
-                    sum += exp2f(z.x - lse2[h]) + exp2f(z.y - lse2[h + 1]) + exp2f(z.z - lse2[h + 2]) + exp2f(z.w - lse2[h + 3]);
+                    float4 z[K];
+#pragma unroll
+                    for (int k = 0; k < K; ++k)
+                        z[k] = t + k * FIN < end ? *reinterpret_cast<const float4*>(x + (int64_t)(t + k * FIN) * group + h) : make_float4(0, 0, 0, 0);
+#pragma unroll
+                    for (int k = 0; k < K; ++k)
+                        sum[k] += exp2_fast(z[k].x - lse2[h]) + exp2_fast(z[k].y - lse2[h + 1]) + exp2_fast(z[k].z - lse2[h + 2]) + exp2_fast(z[k].w - lse2[h + 3]);
                 }
             } else {
-                for (int h = 0; h < some; ++h) sum += exp2f(y[h] - lse2[h]);
+                for (int h = 0; h < some; ++h)
+#pragma unroll
+                    for (int k = 0; k < K; ++k)
+                        if (t + k * FIN < end) sum[k] += exp2_fast(x[(int64_t)(t + k * FIN) * group + h] - lse2[h]);
             }
             // a page of one sequence has one writer per call; sequences that share a page add in any order
-            if ((unsigned)page < (unsigned)c.n_pages)
-                atomicAdd(c.weight + ((int64_t)page * c.n_kv + kvh) * c.page_len + (t & (c.page_len - 1)), sum);
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if ((unsigned)page[k] < (unsigned)c.n_pages)
+                    atomicAdd(c.weight + ((int64_t)page[k] * c.n_kv + kvh) * c.page_len + ((t + k * FIN) & (c.page_len - 1)), sum[k]);
         }
     }
 }
