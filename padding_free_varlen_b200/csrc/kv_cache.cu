@@ -20,29 +20,42 @@ __device__ __forceinline__ bool len_ok(int len, const CacheArgs& c) {
 
 // ------------------------------------------------------------------ append
 
-// 8 consecutive elements of a row as floats.
+// 8 consecutive elements of a row as they are, and as floats.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
-    const uint4 w = *reinterpret_cast<const uint4*>(p);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+struct Raw8 {
+    uint4 w[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ void floats8(const Raw8<T>& r, float (&x)[8]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack2<T>(u[i]);
-        x[2 * i] = f.x, x[2 * i + 1] = f.y;
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+        const uint32_t u[4] = {r.w[i].x, r.w[i].y, r.w[i].z, r.w[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (sizeof(T) == 4) {
+                x[4 * i + j] = __uint_as_float(u[j]);
+            } else {
+                const float2 f = unpack2<T>(u[j]);
+                x[2 * j] = f.x, x[2 * j + 1] = f.y;
+            }
+        }
     }
 }
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&x)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
 
-// The nearest code to x / scale (fp32 quotient, ties to even).
-__device__ __forceinline__ int encode(float x, float scale) {
+// The nearest code to x / scale (fp32 quotient, ties to even), any x and scale.
+__device__ __noinline__ int encode_any(float x, float scale) {
     if (isnan(x)) return 0;
     if (isinf(x)) return x > 0.0f ? 127 : -127;
     if (!(scale > 0.0f)) return 0;
     return __float2int_rn(fminf(fmaxf(__fdiv_rn(x, scale), -127.0f), 127.0f));
+}
+// The same by a product with 1 / scale.  For |x / scale| <= 128 that is off by less than 128 * 2^-22, so
+// that it rounds to the same code unless it lies within 2^-14 of the middle of two: there, and where
+// x is larger or not a number, the quotient decides.
+__device__ __forceinline__ int encode(float x, float scale, float inv) {
+    const float y = x * inv, r = rintf(y);
+    if (!(fabsf(y - r) < 0.5f - 0x1p-14f && fabsf(y) <= 128.0f)) return encode_any(x, scale);
+    return (int)fminf(fmaxf(r, -127.0f), 127.0f);
 }
 
 // New tokens of sequence b: rows start .. start + n - 1 at positions len - n .. len - 1.
@@ -54,15 +67,16 @@ __device__ __forceinline__ bool append_span(const AppendArgs& a, int b, int& sta
 }
 
 constexpr int APPEND_THREADS = 256;
+constexpr int APPEND_HELD = 128 * 128 / 8 / APPEND_THREADS;  // pieces of 8 elements per thread of the largest page
 }  // namespace
 
-// One block = the new tokens of one page of one kv head, keys or values.  The rows are read once
-// for the largest magnitude and again (from the cache next to the SM) to be encoded.
+// One block = the new tokens of one page of one kv head, keys or values.  The rows are read once, into
+// registers: for the largest magnitude, then to be encoded.
 template <typename T>
 __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const AppendArgs a) {
     const CacheArgs& c = a.c;
     if (stopped(c.status)) return;
-    const int tid = threadIdx.x, P = c.page_len, d = c.head_dim;
+    const int tid = threadIdx.x, P = c.page_len, d = c.head_dim, log_p = __ffs(P) - 1;
     if (blockIdx.x == 0 && blockIdx.y == 0 && tid < 32) {
         bool bad = false;
         int s, n, len;
@@ -73,13 +87,13 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const AppendA
     auto count = [&](int i) {
         int s, m, l;
         append_span(a, i, s, m, l);
-        return m > 0 ? (l - 1) / P - (l - m) / P + 1 : 0;
+        return m > 0 ? ((l - 1) >> log_p) - ((l - m) >> log_p) + 1 : 0;
     };
     if (!find_item(c.batch, blockIdx.x, count, b, j)) return;
     append_span(a, b, start, n, len);
     const int head = blockIdx.y >> 1;
     const bool values = blockIdx.y & 1;
-    const int at = (len - n) / P + j;                                      // page of the sequence
+    const int at = ((len - n) >> log_p) + j;                               // page of the sequence
     const int s0 = max(len - n - at * P, 0), s1 = min(len - at * P, P);    // its slots that receive tokens
     const int row0 = start + at * P + s0 - (len - n);
     const int page = c.table[(int64_t)b * c.max_pages + at];
@@ -93,12 +107,24 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const AppendA
     int8_t* codes = (values ? c.v_codes : c.k_codes) + tile * P * d;
     float* scale_at = (values ? c.v_scale : c.k_scale) + tile;
 
-    const int per_row = d / 8, chunks = (s1 - s0) * per_row;
+    const int per_row = d / 8, log_q = __ffs(per_row) - 1, chunks = (s1 - s0) * per_row;
+    Raw8<T> held[APPEND_HELD];
+#pragma unroll
+    for (int r = 0; r < APPEND_HELD; ++r) {
+        const int i = tid + r * APPEND_THREADS;
+        if (i >= chunks) break;
+        const uint4* from = reinterpret_cast<const uint4*>(x + (row0 + (i >> log_q)) * ld + (i & (per_row - 1)) * 8);
+#pragma unroll
+        for (int y = 0; y < (int)sizeof(T) / 2; ++y) held[r].w[y] = from[y];
+    }
+    const float old = *scale_at;  // before any thread may write it
     float amax = 0.0f;
     bool odd = false;
-    for (int i = tid; i < chunks; i += APPEND_THREADS) {
+#pragma unroll
+    for (int r = 0; r < APPEND_HELD; ++r) {
+        if (tid + r * APPEND_THREADS >= chunks) break;
         float f[8];
-        load8<T>(x + (row0 + i / per_row) * ld + (i % per_row) * 8, f);
+        floats8<T>(held[r], f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             if (isfinite(f[e])) amax = fmaxf(amax, fabsf(f[e]));
@@ -106,7 +132,6 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const AppendA
         }
     }
     __shared__ float warp_amax[APPEND_THREADS / 32];
-    const float old = *scale_at;  // before any thread may write it
     amax = warp_max(amax);
     if ((tid & 31) == 0) warp_amax[tid >> 5] = amax;
     if (__syncthreads_or(odd) && tid == 0) status_or(c.status, ENERGON_DEVICE_NONFINITE);
@@ -138,17 +163,21 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const AppendA
         }
     }
     if (tid == 0) *scale_at = scale;
-    for (int i = tid; i < chunks; i += APPEND_THREADS) {
+    const float inv = scale > 0.0f ? 1.0f / scale : INFINITY;  // 0 scale: every element takes the slow way
+#pragma unroll
+    for (int r = 0; r < APPEND_HELD; ++r) {
+        const int i = tid + r * APPEND_THREADS;
+        if (i >= chunks) break;
         float f[8];
-        load8<T>(x + (row0 + i / per_row) * ld + (i % per_row) * 8, f);
+        floats8<T>(held[r], f);
         uint32_t w[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             w[h] = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[h] |= (uint32_t)(encode(f[4 * h + e], scale) & 0xff) << (8 * e);
+            for (int e = 0; e < 4; ++e) w[h] |= (uint32_t)(encode(f[4 * h + e], scale, inv) & 0xff) << (8 * e);
         }
-        *reinterpret_cast<uint2*>(codes + (int64_t)(s0 + i / per_row) * d + (i % per_row) * 8) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2*>(codes + (int64_t)(s0 + (i >> log_q)) * d + (i & (per_row - 1)) * 8) = make_uint2(w[0], w[1]);
     }
     if (!values && c.weight != nullptr)
         for (int s = s0 + tid; s < s1; s += APPEND_THREADS)
@@ -158,7 +187,9 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const AppendA
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t st) {
     if (a.c.batch <= 0 || a.rows <= 0) return cudaSuccess;
     const int some = a.c.batch < a.rows ? a.c.batch : a.rows;
-    const dim3 grid((unsigned)(a.rows / a.c.page_len) + 2u * (unsigned)some, 2 * a.c.n_kv);
+    // a sequence's tokens begin and end inside a page at most, and no page receives less than one
+    const int64_t most = (int64_t)a.rows / a.c.page_len + 2 * (int64_t)some;
+    const dim3 grid((unsigned)(most < a.rows ? most : a.rows), 2 * a.c.n_kv);
     switch (a.dtype) {
     case ENERGON_F32: kv_append_kernel<float><<<grid, APPEND_THREADS, 0, st>>>(a); break;
     case ENERGON_F16: kv_append_kernel<__half><<<grid, APPEND_THREADS, 0, st>>>(a); break;
@@ -172,12 +203,17 @@ cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t st) {
 
 namespace {
 constexpr int SEL_THREADS = 1024;
+constexpr int SEL_WARPS = SEL_THREADS / 32;
+constexpr int HELD = 8;                        // weights that a thread of the selection holds
+constexpr int SPAN = HELD * SEL_THREADS;       // tokens that the block takes at a time
+constexpr int SEL_SMEM = 192 * 1024;           // weights behind the first SPAN wait in shared memory up to here
 constexpr int MOVE_THREADS = 256;
+constexpr int SLICES = 4;                      // blocks that share the rows of a sequence cut in place
 
 // What the selection leaves for the move, per (sequence, kv head): a header and, per kept
 // token, its old position and the factors of its key and value codes.
 struct EvictWs {
-    int4* head;       // {tokens kept, pages at a time, unused, unused}
+    int4* head;       // {tokens kept, anything to move, in place, unused}
     int32_t* src;     // [stride]
     float *by_k, *by_v;
     int stride;
@@ -198,44 +234,24 @@ __device__ __forceinline__ uint32_t order_key(float w) {
     const uint32_t u = __float_as_uint(w + 0.0f);
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
-
-// Exclusive sum over the block of two 16-bit counts in one word; the total goes to `total`.
-__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sums, uint32_t& total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    __syncthreads();  // the previous use of warp_sums is over
-    if (lane == 31) warp_sums[warp] = x;
-    __syncthreads();
-    uint32_t before = 0, sum = 0;
-#pragma unroll
-    for (int w = 0; w < SEL_THREADS / 32; ++w) {
-        if (w == warp) before = sum;
-        sum += warp_sums[w];
-    }
-    total = sum;
-    return before + x - v;
-}
 }  // namespace
 
 // One block = one (sequence, kv head): the kept positions, in order; their weights moved; the
-// new pages' scales.  The smallest kept weight is found digit by digit (8 bits at a time from
-// the top) from counts of the keys that share the digits found so far.
-__global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const EvictArgs a) {
+// new pages' scales.  The smallest kept weight is the largest key T that at least `want` keys
+// reach; it is found two bits at a time from the counts of keys at or above three candidates.
+// Counting needs no histogram, whose bins collide where weights are alike: 3 compares per token and
+// step, from registers.  8 weights per thread are held there; more wait in shared memory.
+__global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const EvictArgs a, int smem_floats) {
     const CacheArgs& c = a.c;
+    extern __shared__ float more[];  // weights SPAN .. SPAN + smem_floats - 1
+    __shared__ int counts[2][3][SEL_WARPS];
+    __shared__ uint32_t taken[HELD][SEL_WARPS];
+    let_next_grid_start();
     if (stopped(c.status)) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int b = blockIdx.y, h = blockIdx.x, P = c.page_len;
+    const int b = blockIdx.y, h = blockIdx.x, P = c.page_len, log_p = __ffs(P) - 1;
     const int item = b * c.n_kv + h;
     const EvictWs ws = evict_ws(a.ws, c.batch * c.n_kv, a.budget);
-    __shared__ uint32_t sums[32];
-    __shared__ int hist[256];
-    __shared__ uint32_t found;
-    __shared__ int left;
     const int32_t* old_row = c.table + (int64_t)b * c.max_pages;
     const int32_t* new_row = a.new_table + (int64_t)b * a.new_max_pages;
 
@@ -244,8 +260,8 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const EvictAr
     const int keep = good ? min(n, a.budget) : 0;
     bool bad = false;
     if (good) {
-        for (int i = tid; i < (n + P - 1) / P; i += SEL_THREADS) bad |= !page_ok(old_row[i], c.n_pages);
-        for (int i = tid; i < (keep + P - 1) / P; i += SEL_THREADS) bad |= !page_ok(new_row[i], c.n_pages);
+        for (int i = tid; i < (n + P - 1) >> log_p; i += SEL_THREADS) bad |= !page_ok(old_row[i], c.n_pages);
+        for (int i = tid; i < (keep + P - 1) >> log_p; i += SEL_THREADS) bad |= !page_ok(new_row[i], c.n_pages);
     }
     bad = __syncthreads_or(bad);
     if (!good || bad || keep == 0) {
@@ -260,77 +276,123 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const EvictAr
     if (in_place && !cut) return;
     int32_t* src = ws.src + (int64_t)item * ws.stride;
     auto weight_at = [&](const int32_t* row, int t) -> float* {
-        return c.weight + (((int64_t)row[t / P] * c.n_kv + h) * P + t % P);
+        return c.weight + (((int64_t)row[t >> log_p] * c.n_kv + h) << log_p) + (t & (P - 1));
     };
+    float held[HELD];
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+        const int t = i * SEL_THREADS + tid;
+        held[i] = t < n ? *weight_at(old_row, t) : 0.0f;
+    }
+    for (int t = SPAN + tid; t < min(n, SPAN + smem_floats); t += SEL_THREADS) more[t - SPAN] = *weight_at(old_row, t);
+    // (a thread reads back its own weights only)
+    auto weight_of = [&](int t) { return t - SPAN < smem_floats ? more[t - SPAN] : *weight_at(old_row, t); };
 
     // tokens 0 .. m-1 compete for `want` places; kept are keys above thr and the first `ties` equal to it
     const int m = cut ? n - a.recent : 0, want = a.budget - a.recent;
     uint32_t thr = 0xffffffffu;
     int ties = 0;
     if (cut && want > 0) {
+        uint32_t key[HELD];
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) key[i] = order_key(held[i]);
         uint32_t prefix = 0;
-        int rest = want;
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = tid; i < 256; i += SEL_THREADS) hist[i] = 0;
-            __syncthreads();
-            for (int t = tid; t < m; t += SEL_THREADS) {
-                const uint32_t k = order_key(*weight_at(old_row, t));
-                if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255u], 1);
+        // steps 0 .. 15 settle two bits each; step 16 counts the keys above the threshold
+        for (int step = 0; step <= 16; ++step) {
+            const int shift = 30 - 2 * step;
+            uint32_t at[3];
+#pragma unroll
+            for (int d = 0; d < 3; ++d) at[d] = step < 16 ? prefix | (uint32_t)(d + 1) << shift : prefix + 1;
+            int x[3] = {0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < HELD; ++i) {
+                if (i * SEL_THREADS + tid >= m) break;
+#pragma unroll
+                for (int d = 0; d < 3; ++d) x[d] += key[i] >= at[d];
             }
-            __syncthreads();
-            if (tid == 0) {
-                int d = 255, r = rest;
-                while (d > 0 && hist[d] < r) r -= hist[d--];
-                found = (uint32_t)d, left = r;
+            for (int t = SPAN + tid; t < m; t += SEL_THREADS) {
+                const uint32_t k = order_key(weight_of(t));
+#pragma unroll
+                for (int d = 0; d < 3; ++d) x[d] += k >= at[d];
             }
-            __syncthreads();
-            prefix |= found << shift;
-            rest = left;
+            int(*part)[SEL_WARPS] = counts[step & 1];
+#pragma unroll
+            for (int d = 0; d < 3; ++d) {
+                const int y = __reduce_add_sync(0xffffffffu, x[d]);
+                if (lane == 0) part[d][warp] = y;
+            }
+            __syncthreads();  // the other half of `counts` is written next: nobody reads it any more
+#pragma unroll
+            for (int d = 0; d < 3; ++d) x[d] = __reduce_add_sync(0xffffffffu, part[d][lane]);
+            if (step < 16) prefix |= (uint32_t)((x[0] >= want) + (x[1] >= want) + (x[2] >= want)) << shift;
+            else ties = prefix == 0xffffffffu ? want : want - x[0];
         }
-        thr = prefix, ties = rest;
+        thr = prefix;
     }
-    uint32_t above = 0, equal = 0;  // kept outright / equal to thr so far
-    for (int t0 = 0; t0 < n; t0 += SEL_THREADS) {
-        const int t = t0 + tid;
-        float w = 0.0f;
-        bool gt = false, eq = false;
-        if (t < n) {
-            w = *weight_at(old_row, t);
-            if (t >= m) gt = true;
-            else if (want > 0) {
-                const uint32_t k = order_key(w);
-                gt = k > thr, eq = k == thr;
+    int above = 0, equal = 0;  // kept outright / equal to thr so far
+    for (int s0 = 0; s0 < n; s0 += SPAN) {
+        if (s0 > 0) {
+#pragma unroll
+            for (int i = 0; i < HELD; ++i) {
+                const int t = s0 + i * SEL_THREADS + tid;
+                held[i] = t < n ? weight_of(t) : 0.0f;
             }
         }
-        uint32_t total;
-        const uint32_t x = block_scan((gt ? 1u : 0u) | (eq ? 0x10000u : 0u), sums, total);
-        const uint32_t e = equal + (x >> 16);
-        // in place: the slot is at or before t, and later rounds read behind it only
-        if (gt || (eq && e < (uint32_t)ties)) {
-            const int slot = (int)(above + (x & 0xffffu) + min(e, (uint32_t)ties));
-            src[slot] = t;
-            *weight_at(new_row, slot) = w;
+        uint32_t gts[HELD], eqs[HELD];
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) {
+            const int t = s0 + i * SEL_THREADS + tid;
+            bool gt = false, eq = false;
+            if (t < n) {
+                if (t >= m) gt = true;
+                else if (want > 0) {
+                    const uint32_t k = order_key(held[i]);
+                    gt = k > thr, eq = k == thr;
+                }
+            }
+            gts[i] = __ballot_sync(0xffffffffu, gt), eqs[i] = __ballot_sync(0xffffffffu, eq);
+            if (lane == 0) taken[i][warp] = __popc(gts[i]) | __popc(eqs[i]) << 16;
         }
-        above += total & 0xffffu, equal += total >> 16;
+        __syncthreads();  // also: this span is read
+        const uint32_t below = (1u << lane) - 1;
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) {
+            const uint32_t v = taken[i][lane];
+            const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? v : 0u), all = __reduce_add_sync(0xffffffffu, v);
+            const bool gt = gts[i] >> lane & 1, eq = eqs[i] >> lane & 1;
+            const int e = equal + (int)(before >> 16) + __popc(eqs[i] & below);
+            // in place: the slot is at or before t, and later spans read behind it only
+            if (gt || (eq && e < ties)) {
+                const int slot = above + (int)(before & 0xffffu) + __popc(gts[i] & below) + min(e, ties);
+                src[slot] = s0 + i * SEL_THREADS + tid;
+                *weight_at(new_row, slot) = held[i];
+            }
+            above += (int)(all & 0xffffu), equal += (int)(all >> 16);
+        }
+        __syncthreads();
     }
-    __syncthreads();
     // Scales: a warp per new page.  In place a page's scale is an input of its own and of earlier
     // pages only, so that a round's scales are written when the round has read.
-    const int pages = (keep + P - 1) / P;
-    for (int p0 = 0; p0 < pages; p0 += SEL_THREADS / 32) {
+    const int pages = (keep + P - 1) >> log_p;
+    for (int p0 = 0; p0 < pages; p0 += SEL_WARPS) {
         const int p = p0 + warp;
-        float mk = 0.0f, mv = 0.0f;
+        float sk[4], sv[4], mk = 0.0f, mv = 0.0f;  // at most 128 tokens a page
         if (p < pages) {
-            for (int i = lane; i < P && p * P + i < keep; i += 32) {
-                const int64_t at = (int64_t)old_row[src[p * P + i] / P] * c.n_kv + h;
-                mk = fmaxf(mk, c.k_scale[at]), mv = fmaxf(mv, c.v_scale[at]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int slot = p * P + i * 32 + lane;
+                const bool live = i * 32 + lane < P && slot < keep;
+                const int64_t at = live ? (int64_t)old_row[src[slot] >> log_p] * c.n_kv + h : 0;
+                sk[i] = live ? c.k_scale[at] : 0.0f, sv[i] = live ? c.v_scale[at] : 0.0f;
+                mk = fmaxf(mk, sk[i]), mv = fmaxf(mv, sv[i]);
             }
             mk = warp_max(mk), mv = warp_max(mv);
-            for (int i = lane; i < P && p * P + i < keep; i += 32) {
-                const int64_t at = (int64_t)old_row[src[p * P + i] / P] * c.n_kv + h;
-                const float sk = c.k_scale[at], sv = c.v_scale[at];
-                ws.by_k[(int64_t)item * ws.stride + p * P + i] = sk > 0.0f ? __fdiv_rn(sk, mk) : 0.0f;
-                ws.by_v[(int64_t)item * ws.stride + p * P + i] = sv > 0.0f ? __fdiv_rn(sv, mv) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int slot = p * P + i * 32 + lane;
+                if (i * 32 + lane >= P || slot >= keep) continue;
+                ws.by_k[(int64_t)item * ws.stride + slot] = sk[i] > 0.0f ? __fdiv_rn(sk[i], mk) : 0.0f;
+                ws.by_v[(int64_t)item * ws.stride + slot] = sv[i] > 0.0f ? __fdiv_rn(sv[i], mv) : 0.0f;
             }
         }
         __syncthreads();
@@ -342,60 +404,68 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const EvictAr
     }
 }
 
-// One block = one new page of one (sequence, kv head), keys or values; in place one block does
-// all pages in order: a page is written after everything that is read from it was read (a kept
-// token's slot is never behind its old position).
+// Codes times the token's factor, rounded.
+__device__ __forceinline__ uint4 scaled_codes(uint4 x, float f) {
+    if (f == 1.0f) return x;
+    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        uint32_t y = 0;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const int q = (int)(int8_t)(w[e] >> (8 * s));
+            y |= (uint32_t)(__float2int_rn(__fmul_rn((float)q, f)) & 0xff) << (8 * s);
+        }
+        w[e] = y;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// One block = one new page of one (sequence, kv head), keys and values; in place SLICES blocks do
+// all pages in order, each its part of the rows' bytes: a page is written after everything that is read
+// from it was read (a kept token's slot is never behind its old position).
 __global__ void __launch_bounds__(MOVE_THREADS) evict_move_kernel(const EvictArgs a) {
     const CacheArgs& c = a.c;
+    wait_for_earlier_grid();
     if (stopped(c.status)) return;
-    const int tid = threadIdx.x, P = c.page_len, d = c.head_dim;
-    const int b = blockIdx.z, h = blockIdx.y >> 1, item = b * c.n_kv + h;
-    const bool values = blockIdx.y & 1;
+    const int tid = threadIdx.x, P = c.page_len, d = c.head_dim, log_p = __ffs(P) - 1;
+    const int b = blockIdx.z, h = blockIdx.y, item = b * c.n_kv + h;
     const EvictWs ws = evict_ws(a.ws, c.batch * c.n_kv, a.budget);
     const int4 head = ws.head[item];
-    const int keep = head.x, pages = (keep + P - 1) / P;
-    if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) a.new_lens[b] = keep;
+    const int keep = head.x, pages = (keep + P - 1) >> log_p;
+    if (blockIdx.x == 0 && h == 0 && tid == 0) a.new_lens[b] = keep;
     if (head.y == 0) return;
     const bool in_place = head.z != 0;
-    if (in_place && blockIdx.x != 0) return;
+    if (in_place ? blockIdx.x >= SLICES : (int)blockIdx.x >= pages) return;
     const int32_t* old_row = c.table + (int64_t)b * c.max_pages;
     const int32_t* new_row = a.new_table + (int64_t)b * a.new_max_pages;
     const int32_t* src = ws.src + (int64_t)item * ws.stride;
-    const float* by = (values ? ws.by_v : ws.by_k) + (int64_t)item * ws.stride;
-    int8_t* codes = values ? c.v_codes : c.k_codes;
-    const int per_row = d / 16;
+    const float *by_k = ws.by_k + (int64_t)item * ws.stride, *by_v = ws.by_v + (int64_t)item * ws.stride;
+    const int pieces = d / 16 / (in_place ? SLICES : 1);          // 16-byte pieces of a row for this block
+    const int first = in_place ? (int)blockIdx.x * pieces : 0, log_q = __ffs(pieces) - 1;
     for (int p = in_place ? 0 : blockIdx.x; p < pages; p += in_place ? 1 : gridDim.x) {
-        const int rows = min(P, keep - p * P);
-        uint4 x[4];  // at most 128 rows x 128 bytes = 4 x 16 bytes per thread
+        const int n = min(P, keep - p * P) * pieces;
+        uint4 k[4], v[4];  // at most 128 rows x 128 bytes = 4 x 16 bytes per thread
+        float fk[4], fv[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int i = tid + r * MOVE_THREADS;
-            if (i < rows * per_row) {
-                const int t = src[p * P + i / per_row];
-                x[r] = *reinterpret_cast<const uint4*>(
-                    codes + (((int64_t)old_row[t / P] * c.n_kv + h) * P + t % P) * d + (i % per_row) * 16);
+            if (i < n) {
+                const int slot = p * P + (i >> log_q), t = src[slot];
+                const int64_t at = ((((int64_t)old_row[t >> log_p] * c.n_kv + h) << log_p) + (t & (P - 1))) * d + (first + (i & (pieces - 1))) * 16;
+                k[r] = *reinterpret_cast<const uint4*>(c.k_codes + at), v[r] = *reinterpret_cast<const uint4*>(c.v_codes + at);
+                fk[r] = by_k[slot], fv[r] = by_v[slot];
             }
         }
         if (in_place) __syncthreads();
-        int8_t* to = codes + ((int64_t)new_row[p] * c.n_kv + h) * P * d;
+        const int64_t to = (((int64_t)new_row[p] * c.n_kv + h) << log_p) * d;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int i = tid + r * MOVE_THREADS;
-            if (i < rows * per_row) {
-                const float f = by[p * P + i / per_row];
-                uint32_t w[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    uint32_t y = 0;
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        const int q = (int)(int8_t)(w[e] >> (8 * s));
-                        y |= (uint32_t)(__float2int_rn(__fmul_rn((float)q, f)) & 0xff) << (8 * s);
-                    }
-                    w[e] = y;
-                }
-                *reinterpret_cast<uint4*>(to + (int64_t)(i / per_row) * d + (i % per_row) * 16) =
-                    make_uint4(w[0], w[1], w[2], w[3]);
+            if (i < n) {
+                const int64_t at = to + (int64_t)(i >> log_q) * d + (first + (i & (pieces - 1))) * 16;
+                *reinterpret_cast<uint4*>(c.k_codes + at) = scaled_codes(k[r], fk[r]);
+                *reinterpret_cast<uint4*>(c.v_codes + at) = scaled_codes(v[r], fv[r]);
             }
         }
         if (in_place) __syncthreads();
@@ -409,13 +479,17 @@ size_t cache_evict_ws_bytes(int batch, int n_kv, int budget) {
 
 cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t st) {
     if (a.c.batch <= 0) return cudaSuccess;
-    evict_select_kernel<<<dim3(a.c.n_kv, a.c.batch), SEL_THREADS, 0, st>>>(a);
-    cudaError_t e = cudaGetLastError();
+    // weights behind the first SPAN tokens, as far as shared memory holds them
+    const int behind = a.c.max_len > SPAN ? a.c.max_len - SPAN : 0;
+    const int floats = behind < SEL_SMEM / 4 ? behind : SEL_SMEM / 4;
+    cudaError_t e = floats * 4 > 40 * 1024 ? prepare_smem((const void*)evict_select_kernel, SEL_SMEM) : cudaSuccess;
+    if (e != cudaSuccess) return e;
+    evict_select_kernel<<<dim3(a.c.n_kv, a.c.batch), SEL_THREADS, floats * 4, st>>>(a, floats);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int most = a.budget < a.c.max_len ? a.budget : a.c.max_len;
-    const unsigned pages = (unsigned)((most + a.c.page_len - 1) / a.c.page_len);
-    evict_move_kernel<<<dim3(pages > 0 ? pages : 1, 2 * a.c.n_kv, a.c.batch), MOVE_THREADS, 0, st>>>(a);
-    return cudaGetLastError();
+    const int pages = (most + a.c.page_len - 1) / a.c.page_len;
+    return launch_early(evict_move_kernel, dim3(pages > SLICES ? pages : SLICES, a.c.n_kv, a.c.batch), MOVE_THREADS, st, a);
 }
 
 }  // namespace energon
