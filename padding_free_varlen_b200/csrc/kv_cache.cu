@@ -49,13 +49,29 @@ __device__ __noinline__ int encode_any(float x, float scale) {
     if (!(scale > 0.0f)) return 0;
     return __float2int_rn(fminf(fmaxf(__fdiv_rn(x, scale), -127.0f), 127.0f));
 }
-// The same by a product with 1 / scale.  For |x / scale| <= 128 that is off by less than 128 * 2^-22, so
-// that it rounds to the same code unless it lies within 2^-14 of the middle of two: there, and where
-// x is larger or not a number, the quotient decides.
-__device__ __forceinline__ int encode(float x, float scale, float inv) {
-    const float y = x * inv, r = rintf(y);
-    if (!(fabsf(y - r) < 0.5f - 0x1p-14f && fabsf(y) <= 128.0f)) return encode_any(x, scale);
-    return (int)fminf(fmaxf(r, -127.0f), 127.0f);
+// Codes of 8 finite elements with |x| <= 127 scale (1 + 2^-22), 2^-90 < scale < 2^120, from
+// inv = 1 / scale rounded to nearest.  The quotient is made exact in its last place by two residual
+// corrections q + (x - q scale) inv (P. Markstein, Computation of elementary functions on the IBM RISC
+// System/6000 processor, 1990: the second one rounds a quotient that is good to its last place
+// correctly).  A test of nearness to the middle of two codes would not do: bf16 elements over a page's
+// largest lie there once in some hundred.  Adding 1.5 * 2^23 rounds to the code, left in the low byte.
+__device__ __forceinline__ uint2 encode8(const float (&x)[8], uint64_t neg_scale, uint64_t inv) {
+    constexpr float MAGIC = 12582912.0f;
+    uint32_t byte[8];
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        const uint64_t v = two(x[e], x[e + 1]);
+        uint64_t q = mul2(v, inv);
+        q = fma2(fma2(q, neg_scale, v), inv, q);
+        q = fma2(fma2(q, neg_scale, v), inv, q);
+        const float2 f = one_by_one(add2(q, two(MAGIC, MAGIC)));
+        byte[e] = __float_as_uint(f.x), byte[e + 1] = __float_as_uint(f.y);
+    }
+    uint32_t w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        w[h] = __byte_perm(__byte_perm(byte[4 * h], byte[4 * h + 1], 0x0040), __byte_perm(byte[4 * h + 2], byte[4 * h + 3], 0x0040), 0x5410);
+    return make_uint2(w[0], w[1]);
 }
 
 // New tokens of sequence b: rows start .. start + n - 1 at positions len - n .. len - 1.
@@ -73,7 +89,7 @@ constexpr int APPEND_HELD = 128 * 128 / 8 / APPEND_THREADS;  // pieces of 8 elem
 // One block = the new tokens of one page of one kv head, keys or values.  The rows are read once, into
 // registers: for the largest magnitude, then to be encoded.
 template <typename T>
-__global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(APPEND_THREADS, sizeof(T) == 4 ? 2 : 4) kv_append_kernel(const AppendArgs a) {
     const CacheArgs& c = a.c;
     if (stopped(c.status)) return;
     const int tid = threadIdx.x, P = c.page_len, d = c.head_dim, log_p = __ffs(P) - 1;
@@ -91,8 +107,6 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const AppendA
     };
     if (!find_item(c.batch, blockIdx.x, count, b, j)) return;
     append_span(a, b, start, n, len);
-    const int head = blockIdx.y >> 1;
-    const bool values = blockIdx.y & 1;
     const int at = ((len - n) >> log_p) + j;                               // page of the sequence
     const int s0 = max(len - n - at * P, 0), s1 = min(len - at * P, P);    // its slots that receive tokens
     const int row0 = start + at * P + s0 - (len - n);
@@ -101,87 +115,118 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const AppendA
         if (tid == 0) status_or(c.status, ENERGON_DEVICE_BAD_PAGE);
         return;
     }
-    const T* x = static_cast<const T*>(values ? a.v : a.k) + (int64_t)head * d;
-    const int64_t ld = values ? a.ld_v : a.ld_k;
-    const int64_t tile = (int64_t)page * c.n_kv + head;
-    int8_t* codes = (values ? c.v_codes : c.k_codes) + tile * P * d;
-    float* scale_at = (values ? c.v_scale : c.k_scale) + tile;
+    __shared__ float warp_amax[2][APPEND_THREADS / 32];
+    int round = 0;
+    for (int part = blockIdx.y; part < 2 * c.n_kv; part += gridDim.y, ++round) {  // keys and values of every head
+        const int head = part >> 1;
+        const bool values = part & 1;
+        const T* x = static_cast<const T*>(values ? a.v : a.k) + (int64_t)head * d;
+        const int64_t ld = values ? a.ld_v : a.ld_k;
+        const int64_t tile = (int64_t)page * c.n_kv + head;
+        int8_t* codes = (values ? c.v_codes : c.k_codes) + tile * P * d;
+        float* scale_at = (values ? c.v_scale : c.k_scale) + tile;
 
-    const int per_row = d / 8, log_q = __ffs(per_row) - 1, chunks = (s1 - s0) * per_row;
-    Raw8<T> held[APPEND_HELD];
+        const int per_row = d / 8, log_q = __ffs(per_row) - 1, chunks = (s1 - s0) * per_row;
+        Raw8<T> held[APPEND_HELD];
 #pragma unroll
-    for (int r = 0; r < APPEND_HELD; ++r) {
-        const int i = tid + r * APPEND_THREADS;
-        if (i >= chunks) break;
-        const uint4* from = reinterpret_cast<const uint4*>(x + (row0 + (i >> log_q)) * ld + (i & (per_row - 1)) * 8);
+        for (int r = 0; r < APPEND_HELD; ++r) {
+            const int i = tid + r * APPEND_THREADS;
+            if (i >= chunks) break;
+            const uint4* from = reinterpret_cast<const uint4*>(x + (row0 + (i >> log_q)) * ld + (i & (per_row - 1)) * 8);
 #pragma unroll
-        for (int y = 0; y < (int)sizeof(T) / 2; ++y) held[r].w[y] = from[y];
-    }
-    const float old = *scale_at;  // before any thread may write it
-    float amax = 0.0f;
-    bool odd = false;
-#pragma unroll
-    for (int r = 0; r < APPEND_HELD; ++r) {
-        if (tid + r * APPEND_THREADS >= chunks) break;
-        float f[8];
-        floats8<T>(held[r], f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (isfinite(f[e])) amax = fmaxf(amax, fabsf(f[e]));
-            else odd = true;
+            for (int y = 0; y < (int)sizeof(T) / 2; ++y) held[r].w[y] = from[y];
         }
-    }
-    __shared__ float warp_amax[APPEND_THREADS / 32];
-    amax = warp_max(amax);
-    if ((tid & 31) == 0) warp_amax[tid >> 5] = amax;
-    if (__syncthreads_or(odd) && tid == 0) status_or(c.status, ENERGON_DEVICE_NONFINITE);
+        const float old = *scale_at;  // before any thread may write it
+        // Magnitudes compare like their bits; of 16-bit types two at a time.
+        uint32_t most[2] = {0, 0};
 #pragma unroll
-    for (int w = 0; w < APPEND_THREADS / 32; ++w) amax = fmaxf(amax, warp_amax[w]);
-    float need = amax * (1.0f / 127.0f);
-    if (need < FLT_MIN) need = 0.0f;
-    float scale = need;
-    if (s0 > 0) {  // the page holds earlier tokens
-        int up = 0;
-        if (old > 0.0f) {
-            if (need > old) {
-                int e_old, e_need;
-                const float m_old = frexpf(old, &e_old), m_need = frexpf(need, &e_need);
-                up = e_need - e_old + (m_need > m_old ? 1 : 0);
-            }
-            scale = ldexpf(old, up);
-        }
-        if (up > 0) {
-            const float by = ldexpf(1.0f, -up);
-            for (int i = tid; i < P * d / 4; i += APPEND_THREADS) {
-                const int slot = i * 4 / d;
-                if (slot >= s0 && slot < s1) continue;
-                char4 q = reinterpret_cast<char4*>(codes)[i];
-                q.x = (signed char)__float2int_rn(q.x * by), q.y = (signed char)__float2int_rn(q.y * by);
-                q.z = (signed char)__float2int_rn(q.z * by), q.w = (signed char)__float2int_rn(q.w * by);
-                reinterpret_cast<char4*>(codes)[i] = q;
+        for (int r = 0; r < APPEND_HELD; ++r) {
+            if (tid + r * APPEND_THREADS >= chunks) break;
+#pragma unroll
+            for (int y = 0; y < (int)sizeof(T) / 2; ++y) {
+                const uint32_t u[4] = {held[r].w[y].x, held[r].w[y].y, held[r].w[y].z, held[r].w[y].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (sizeof(T) == 4) most[e & 1] = max(most[e & 1], u[e] & 0x7fffffffu);
+                    else most[e & 1] = __vmaxu2(most[e & 1], u[e] & 0x7fff7fffu);
+                }
             }
         }
-    }
-    if (tid == 0) *scale_at = scale;
-    const float inv = scale > 0.0f ? 1.0f / scale : INFINITY;  // 0 scale: every element takes the slow way
-#pragma unroll
-    for (int r = 0; r < APPEND_HELD; ++r) {
-        const int i = tid + r * APPEND_THREADS;
-        if (i >= chunks) break;
-        float f[8];
-        floats8<T>(held[r], f);
-        uint32_t w[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            w[h] = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[h] |= (uint32_t)(encode(f[4 * h + e], scale, inv) & 0xff) << (8 * e);
+        float amax;
+        if constexpr (sizeof(T) == 4) {
+            amax = __uint_as_float(max(most[0], most[1]));
+        } else {
+            const float2 f = unpack2<T>(__vmaxu2(most[0], most[1]));
+            amax = isnan(f.x) || isnan(f.y) ? NAN : fmaxf(f.x, f.y);
         }
-        *reinterpret_cast<uint2*>(codes + (int64_t)(s0 + (i >> log_q)) * d + (i & (per_row - 1)) * 8) = make_uint2(w[0], w[1]);
+        const bool odd = !isfinite(amax);
+        if (odd) {  // a value that is not finite does not count
+            amax = 0.0f;
+#pragma unroll
+            for (int r = 0; r < APPEND_HELD; ++r) {
+                if (tid + r * APPEND_THREADS >= chunks) break;
+                float f[8];
+                floats8<T>(held[r], f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (isfinite(f[e])) amax = fmaxf(amax, fabsf(f[e]));
+            }
+        }
+        amax = warp_max(amax);
+        if ((tid & 31) == 0) warp_amax[round & 1][tid >> 5] = amax;
+        const bool any_odd = __syncthreads_or(odd);
+        if (any_odd && tid == 0) status_or(c.status, ENERGON_DEVICE_NONFINITE);
+#pragma unroll
+        for (int w = 0; w < APPEND_THREADS / 32; ++w) amax = fmaxf(amax, warp_amax[round & 1][w]);
+        float need = amax * (1.0f / 127.0f);
+        if (need < FLT_MIN) need = 0.0f;
+        float scale = need;
+        if (s0 > 0) {  // the page holds earlier tokens
+            int up = 0;
+            if (old > 0.0f) {
+                if (need > old) {
+                    int e_old, e_need;
+                    const float m_old = frexpf(old, &e_old), m_need = frexpf(need, &e_need);
+                    up = e_need - e_old + (m_need > m_old ? 1 : 0);
+                }
+                scale = ldexpf(old, up);
+            }
+            if (up > 0) {
+                const float by = ldexpf(1.0f, -up);
+                for (int i = tid; i < P * d / 4; i += APPEND_THREADS) {
+                    const int slot = i * 4 / d;
+                    if (slot >= s0 && slot < s1) continue;
+                    char4 q = reinterpret_cast<char4*>(codes)[i];
+                    q.x = (signed char)__float2int_rn(q.x * by), q.y = (signed char)__float2int_rn(q.y * by);
+                    q.z = (signed char)__float2int_rn(q.z * by), q.w = (signed char)__float2int_rn(q.w * by);
+                    reinterpret_cast<char4*>(codes)[i] = q;
+                }
+            }
+        }
+        if (tid == 0) *scale_at = scale;
+        const bool plain = !any_odd && scale > 0x1p-90f && scale < 0x1p120f;
+        const float inv = plain ? __frcp_rn(scale) : 0.0f;
+#pragma unroll
+        for (int r = 0; r < APPEND_HELD; ++r) {
+            const int i = tid + r * APPEND_THREADS;
+            if (i >= chunks) break;
+            float f[8];
+            floats8<T>(held[r], f);
+            uint2 w;
+            if (plain) {
+                w = encode8(f, two(-scale, -scale), two(inv, inv));
+            } else {
+                uint32_t y[2] = {0, 0};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e >> 2] |= (uint32_t)(encode_any(f[e], scale) & 0xff) << (8 * (e & 3));
+                w = make_uint2(y[0], y[1]);
+            }
+            *reinterpret_cast<uint2*>(codes + (int64_t)(s0 + (i >> log_q)) * d + (i & (per_row - 1)) * 8) = w;
+        }
+        if (!values && c.weight != nullptr)
+            for (int s = s0 + tid; s < s1; s += APPEND_THREADS)
+                c.weight[tile * P + s] = a.weights ? a.weights[(int64_t)head * a.rows + row0 + s - s0] : 0.0f;
     }
-    if (!values && c.weight != nullptr)
-        for (int s = s0 + tid; s < s1; s += APPEND_THREADS)
-            c.weight[tile * P + s] = a.weights ? a.weights[(int64_t)head * a.rows + row0 + s - s0] : 0.0f;
 }
 
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t st) {
@@ -189,7 +234,13 @@ cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t st) {
     const int some = a.c.batch < a.rows ? a.c.batch : a.rows;
     // a sequence's tokens begin and end inside a page at most, and no page receives less than one
     const int64_t most = (int64_t)a.rows / a.c.page_len + 2 * (int64_t)some;
-    const dim3 grid((unsigned)(most < a.rows ? most : a.rows), 2 * a.c.n_kv);
+    const int64_t pages = most < a.rows ? most : a.rows;
+    // A block finds its page by a chain of loads; where pages are many it takes several heads of it (about two
+    // rounds of blocks on the SMs).  16 prompts, 16 thousand tokens in all: 35 us, of which memory would
+    // take 15; 48 single tokens: 7 us, a block for each page and head.
+    int64_t parts = (4 * 148 * 2 + pages - 1) / pages;
+    if (parts > 2 * a.c.n_kv) parts = 2 * a.c.n_kv;
+    const dim3 grid((unsigned)pages, (unsigned)parts);
     switch (a.dtype) {
     case ENERGON_F32: kv_append_kernel<float><<<grid, APPEND_THREADS, 0, st>>>(a); break;
     case ENERGON_F16: kv_append_kernel<__half><<<grid, APPEND_THREADS, 0, st>>>(a); break;
@@ -303,13 +354,16 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const EvictAr
             uint32_t at[3];
 #pragma unroll
             for (int d = 0; d < 3; ++d) at[d] = step < 16 ? prefix | (uint32_t)(d + 1) << shift : prefix + 1;
-            int x[3] = {0, 0, 0};
+            int x[3];
+            uint32_t three = 0;  // at most HELD * 32 a warp: 10 bits each
 #pragma unroll
             for (int i = 0; i < HELD; ++i) {
                 if (i * SEL_THREADS + tid >= m) break;
-#pragma unroll
-                for (int d = 0; d < 3; ++d) x[d] += key[i] >= at[d];
+                three += (key[i] >= at[0] ? 1u : 0u) + (key[i] >= at[1] ? 1u << 10 : 0u) + (key[i] >= at[2] ? 1u << 20 : 0u);
             }
+            three = __reduce_add_sync(0xffffffffu, three);
+#pragma unroll
+            for (int d = 0; d < 3; ++d) x[d] = lane == 0 ? (int)(three >> 10 * d & 1023u) : 0;
             for (int t = SPAN + tid; t < m; t += SEL_THREADS) {
                 const uint32_t k = order_key(weight_of(t));
 #pragma unroll
@@ -318,7 +372,7 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const EvictAr
             int(*part)[SEL_WARPS] = counts[step & 1];
 #pragma unroll
             for (int d = 0; d < 3; ++d) {
-                const int y = __reduce_add_sync(0xffffffffu, x[d]);
+                const int y = m > SPAN ? __reduce_add_sync(0xffffffffu, x[d]) : x[d];
                 if (lane == 0) part[d][warp] = y;
             }
             __syncthreads();  // the other half of `counts` is written next: nobody reads it any more
