@@ -40,15 +40,19 @@ template <int HD, int NT>
 struct TCfg {
     static constexpr int QT = HD / 64 * QBOX;                // bytes of a Q tile
     static constexpr int KT = HD * BN * 2;                   // bytes of a K or V block
-    static constexpr int RING = NT == 2 ? (HD == 128 ? 5 : 8) : 2;  // buffers of K, and of V
-    static constexpr int SMEM = NT * QT + 2 * RING * KT + 1024;
+    // buffers of K and of V; the Q tiles have two
+    static constexpr int RK = NT == 2 ? (HD == 128 ? 3 : 6) : (HD == 128 ? 2 : 4);
+    static constexpr int RV = NT == 2 ? (HD == 128 ? 3 : 6) : (HD == 128 ? 1 : 4);
+    static constexpr int TILES = 2 * NT * QT + (RK + RV) * KT;
     static constexpr int THREADS = NT * 128 + 128;
     static constexpr int SCAN = NT == 2 ? 32 : 64;           // threads that scan V
     static constexpr int O_COL = NT * 2 * BN;                // S takes two buffers per tile
     static constexpr int TMEM = NT == 2 ? 512 : 256;
     static constexpr int CTAS = NT == 2 ? 1 : 2;
     static constexpr int SCANS = NT * BM / BN;               // most blocks that cross a diagonal
+    static constexpr int READERS = NT * 4 + NT + SCAN / 32;  // warps that follow the items
 };
+constexpr int ITEMS = 4;  // items that the loader announces ahead
 
 // O (or S) += A B with A (M = 128 rows, 16-bit, two per 32-bit column) read from TMEM.
 __device__ __forceinline__ void umma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
@@ -68,7 +72,67 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
         "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
-__device__ __forceinline__ void wg_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+// Barrier of a tile's 128 softmax threads; true in all of them if `ok` is in all.
+__device__ __forceinline__ bool tile_sync(int id, bool ok) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %2, 0;\n\t"
+        "bar.red.and.pred q, %1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"((uint32_t)ok)
+        : "memory");
+    return r != 0;
+}
+// Barrier of the threads that scan; true in all of them if `ok` is in all.
+template <int N>
+__device__ __forceinline__ bool scan_sync(bool ok) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.and.pred q, 8, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)ok), "n"(N)
+        : "memory");
+    return r != 0;
+}
+// Three positions below 256 of 9 bits each; 256: none.  note_bad lowers one of them.
+constexpr uint32_t NONE_BAD = 256u | 256u << 9 | 256u << 18;
+__device__ __forceinline__ void note_bad(uint32_t* word, int kind, int at) {
+    uint32_t old = *reinterpret_cast<volatile uint32_t*>(word);
+    while ((int)(old >> 9 * kind & 511u) > at) {
+        const uint32_t want = (old & ~(511u << 9 * kind)) | (uint32_t)at << 9 * kind;
+        const uint32_t was = atomicCAS(word, old, want);
+        if (was == old) break;
+        old = was;
+    }
+}
+// Asks for the place of a block that has not started (it will not start any more if granted): the
+// hardware's own order of blocks, without their start.
+__device__ __forceinline__ void ask_next_block(uint4* answer, uint64_t* bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     smem_u32(answer)),
+                 "r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ bool next_block(const uint4* answer, int& x, int& y) {
+    uint32_t got;
+    asm volatile(
+        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 r, [%3];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::y.b32.b128 %2, r;\n\t}"
+        : "=r"(got), "=&r"(x), "=&r"(y)
+        : "r"(smem_u32(answer))
+        : "memory");
+    return got != 0;
+}
 }  // namespace
 
 // Maximum of N scores.
@@ -91,58 +155,86 @@ struct PromptTcArgs {
     float c;         // scale * log2(e)
 };
 
+// What a block's warps share beside the tiles.
+template <int HD, int NT>
+struct Aux {
+    using C = TCfg<HD, NT>;
+    uint64_t q_full[2], q_free[2], o_done[NT], o_full[NT], drain[NT], s_full[NT][2], p_full[NT][2];
+    uint64_t k_full[C::RK], k_empty[C::RK], v_full[C::RV], v_empty[C::RV];
+    uint64_t v_in[C::RV];     // a block that is scanned has landed in this buffer
+    uint64_t v_ok[C::SCANS];  // an item's first, second, ... such block is scanned
+    uint64_t item_full[ITEMS], item_empty[ITEMS], answer_bar, pad;
+    int4 items[ITEMS];
+    uint4 answer;
+    uint32_t tmem_slot;
+    int dead, odd;       // odd: 1 + the last item with a value that is not finite in a scanned block
+    uint32_t first[HD];  // there: the first keys whose value in this column is +inf, -inf, NaN
+};
+
+// One work item of a block.
+struct PromptItem {
+    int start, n, blk, head0;  // first row and length of the sequence, tile, first query head; n = 0: no more items
+    int pair, rows;            // rows that an item's tiles cover
+    __device__ __forceinline__ int q0(int i) const { return blk * rows + (pair ? 0 : i * BM); }
+    __device__ __forceinline__ int head(int i) const { return head0 + (pair ? i : 0); }
+    // key blocks of tile i (0: the tile has no queries), and of the item
+    __device__ __forceinline__ int blocks(int i) const { return q0(i) < n ? (min(n, q0(i) + BM) + BN - 1) / BN : 0; }
+    template <int NT>
+    __device__ __forceinline__ int all_blocks() const { return NT == 1 ? blocks(0) : max(blocks(0), blocks(1)); }
+    __device__ __forceinline__ int scan0() const { return q0(0) / BN; }  // first block with keys behind a query
+};
+
 template <typename T, int HD, int NT>
 __global__ void __launch_bounds__(TCfg<HD, NT>::THREADS, TCfg<HD, NT>::CTAS)
 prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
                  const PromptTcArgs a) {
     using C = TCfg<HD, NT>;
-    extern __shared__ uint8_t raw[];
-    __shared__ uint64_t q_full[NT], s_full[NT][2], p_full[NT][2], o_done[NT], o_full[NT], drain[NT];
-    __shared__ uint64_t k_full[C::RING], k_empty[C::RING], v_full[C::RING], v_empty[C::RING];
-    __shared__ uint64_t v_in[C::SCANS], v_ok[C::SCANS];  // blocks that are scanned: landed, scanned (used once each)
-    __shared__ uint32_t tmem_slot;
-    __shared__ int dead, odd;
-    __shared__ int first[3][HD];  // first key whose value in this column is +inf, -inf, NaN
+    extern __shared__ __align__(1024) uint8_t base[];  // the tiles, swizzled in units of 1024 bytes, then Aux
+    Aux<HD, NT>& aux = *reinterpret_cast<Aux<HD, NT>*>(base + C::TILES);
+    auto& q_full = aux.q_full;
+    auto& q_free = aux.q_free;
+    auto& o_done = aux.o_done;
+    auto& o_full = aux.o_full;
+    auto& drain = aux.drain;
+    auto& s_full = aux.s_full;
+    auto& p_full = aux.p_full;
+    auto& k_full = aux.k_full;
+    auto& k_empty = aux.k_empty;
+    auto& v_full = aux.v_full;
+    auto& v_empty = aux.v_empty;
+    auto& v_in = aux.v_in;
+    auto& v_ok = aux.v_ok;
+    auto& item_full = aux.item_full;
+    auto& item_empty = aux.item_empty;
+    auto& answer_bar = aux.answer_bar;
+    auto& items = aux.items;
+    auto& answer = aux.answer;
+    auto& tmem_slot = aux.tmem_slot;
+    auto& dead = aux.dead;
+    auto& odd = aux.odd;
+    auto& first = aux.first;
     const PromptArgs& p = a.p;
     if (stopped(p.status)) return;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const int64_t item = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;  // heads pass by first
-    if (item == 0 && tid < 32) check_rows(p.cu, p.batch, p.rows, p.status);
-
-    // ---- which queries
     const int tile_rows = NT == 2 && !a.pair_heads ? 2 * BM : BM;
-    int b, blk, start, n;
-    auto count = [&](int i) {
-        int s, len;
-        seq_rows(p.cu, i, p.rows, s, len);
-        return (len + tile_rows - 1) / tile_rows;
-    };
-    if (!find_item(p.batch, (int)(item / a.head_steps), count, b, blk)) return;
-    seq_rows(p.cu, b, p.rows, start, n);
-    blk = (n + tile_rows - 1) / tile_rows - 1 - blk;  // the longest rows first
-    const int head0 = (int)(item % a.head_steps) * (a.pair_heads ? 2 : 1);
-    const int kvh = head0 / (p.n_heads / p.n_kv);
-    auto q0_of = [&](int i) { return blk * tile_rows + (a.pair_heads ? 0 : i * BM); };
-    auto head_of = [&](int i) { return head0 + (a.pair_heads ? i : 0); };
-    // key blocks of tile i (0: the tile has no queries)
-    auto blocks_of = [&](int i) { return q0_of(i) < n ? (min(n, q0_of(i) + BM) + BN - 1) / BN : 0; };
-    const int nb0 = blocks_of(0), nb1 = NT == 2 ? blocks_of(NT - 1) : 0, nb = max(nb0, nb1);
-    const int scan0 = q0_of(0) / BN;  // first block with keys behind a query
 
-    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* ring_k = base + NT * C::QT;
-    uint8_t* ring_v = ring_k + C::RING * C::KT;
-    for (int i = tid; i < 3 * HD; i += C::THREADS) (&first[0][0])[i] = 0x7fffffff;
+    uint8_t* ring_k = base + 2 * NT * C::QT;
+    uint8_t* ring_v = ring_k + C::RK * C::KT;
+    auto q_tile = [&](int k, int i) { return base + ((k & 1) * NT + i) * C::QT; };  // of item k
+    for (int i = tid; i < HD; i += C::THREADS) first[i] = NONE_BAD;
     if (tid == 0) {
+        for (int i = 0; i < 2; ++i) mbar_init(&q_full[i], 1), mbar_init(&q_free[i], NT * 128);
         for (int i = 0; i < NT; ++i) {
-            mbar_init(&q_full[i], 1), mbar_init(&o_done[i], 1), mbar_init(&o_full[i], 1), mbar_init(&drain[i], 1);
+            mbar_init(&o_done[i], 1), mbar_init(&o_full[i], 1), mbar_init(&drain[i], 1);
             for (int y = 0; y < 2; ++y) mbar_init(&s_full[i][y], 1), mbar_init(&p_full[i][y], 128);
         }
-        for (int i = 0; i < C::RING; ++i)
-            mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], NT), mbar_init(&v_full[i], 1), mbar_init(&v_empty[i], NT);
-        for (int i = 0; i < C::SCANS; ++i) mbar_init(&v_in[i], 1), mbar_init(&v_ok[i], C::SCAN);
-        dead = 0, odd = 0;
+        for (int i = 0; i < C::RK; ++i) mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], NT);
+        for (int i = 0; i < C::RV; ++i) mbar_init(&v_full[i], 1), mbar_init(&v_empty[i], NT), mbar_init(&v_in[i], 1);
+        for (int i = 0; i < C::SCANS; ++i) mbar_init(&v_ok[i], C::SCAN);
+        for (int i = 0; i < ITEMS; ++i) mbar_init(&item_full[i], 1), mbar_init(&item_empty[i], C::READERS);
+        mbar_init(&answer_bar, 1);
+        dead = smem_u32(base) % 1024 != 0, odd = 0;
         fence_mbar_init();
     }
     if (warp == NT * 4) {
@@ -158,84 +250,179 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         *reinterpret_cast<volatile int*>(&dead) = 1;
         return false;
     };
+    // TMEM is read, and work is issued, by whole warps: their lanes give up together
+    auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+    PromptItem it;
+    it.pair = a.pair_heads, it.rows = tile_rows;
+    // Item k of this block; false where a wait ran out.  `leave`: this warp needs it no more.
+    auto read_item = [&](int k, PromptItem& to, bool leave) {
+        const int at = k % ITEMS;
+        const volatile int4& v = items[at];
+        const int4 w = make_int4(v.x, v.y, v.z, v.w);
+        to.start = w.x, to.n = w.y, to.blk = w.z, to.head0 = w.w;
+        __syncwarp();
+        if (leave && lane == 0) mbar_arrive(&item_empty[at]);
+    };
+    auto item_there = [&](int k) { return wait_warp(&item_full[k % ITEMS], (k / ITEMS) & 1); };
 
     if (warp == NT * 4) {
-        if (lane == 0) {
-            // ---- loader: Q, then K(0), K(1), V(0), K(2), V(1), ...
-            for (int i = 0; i < NT; ++i) {
-                if (i > 0 && nb1 == 0) break;
-                mbar_arrive_expect_tx(&q_full[i], C::QT);
-                for (int h = 0; h < HD / 64; ++h)
-                    tma_load_2d(base + i * C::QT + h * QBOX, &tm_q, &q_full[i], head_of(i) * HD + 64 * h, start + q0_of(i));
+        // ---- loader: announces the items, loads Q, then K(0), K(1), V(0), K(2), V(1), ... of each
+        int x = blockIdx.x, y = blockIdx.y, k = 0, nk = 0, nv = 0, asked = 0;
+        uint32_t ins = 0;  // bit i: parity of v_in[i]'s next use
+        bool ok = dead == 0, more = true;
+        auto announce = [&](int4 w) {
+            const int at = k % ITEMS;
+            if (k >= ITEMS) ok = wait_warp(&item_empty[at], (k / ITEMS - 1) & 1);
+            if (ok && lane == 0) {
+                items[at] = w;
+                mbar_arrive(&item_full[at]);
             }
-            int nk = 0, nv = 0;  // blocks asked for
-            for (int x = 0; x < 2 * nb; ++x) {
-                const bool keys = nk < nb && nk - nv < 2;
-                const int kb = keys ? nk : nv, at = kb % C::RING;
-                if (kb >= C::RING && !wait(keys ? &k_empty[at] : &v_empty[at], (kb / C::RING - 1) & 1)) break;
-                uint64_t* bar = keys ? &k_full[at] : &v_full[at];
-                if (!keys && kb >= scan0) {  // the scan waits for this one alone
-                    mbar_arrive(bar);
-                    bar = &v_in[kb - scan0];
+            __syncwarp();
+        };
+        while (ok && more) {
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&answer_bar, 16);
+                ask_next_block(&answer, &answer_bar);
+            }
+            const int64_t lin = (int64_t)y * gridDim.x + x;  // heads pass by first
+            if (lin == 0) check_rows(p.cu, p.batch, p.rows, p.status);
+            int b, blk;
+            auto count = [&](int i) {
+                int s, len;
+                seq_rows(p.cu, i, p.rows, s, len);
+                return (len + tile_rows - 1) / tile_rows;
+            };
+            if (find_item(p.batch, (int)(lin / a.head_steps), count, b, blk)) {
+                seq_rows(p.cu, b, p.rows, it.start, it.n);
+                it.blk = (it.n + tile_rows - 1) / tile_rows - 1 - blk;  // the longest rows first
+                it.head0 = (int)(lin % a.head_steps) * (a.pair_heads ? 2 : 1);
+                announce(make_int4(it.start, it.n, it.blk, it.head0));
+                const int kvh = it.head0 / (p.n_heads / p.n_kv), nb = it.all_blocks<NT>(), scan0 = it.scan0();
+                if (ok && k >= 2) ok = wait_warp(&q_free[k & 1], ((k >> 1) - 1) & 1);
+                if (ok && elect_one()) {
+                    const int tiles = NT == 2 && it.blocks(NT - 1) > 0 ? NT : 1;
+                    mbar_arrive_expect_tx(&q_full[k & 1], tiles * C::QT);
+                    for (int i = 0; i < tiles; ++i)
+                        for (int h = 0; h < HD / 64; ++h)
+                            tma_load_2d(q_tile(k, i) + h * QBOX, &tm_q, &q_full[k & 1], it.head(i) * HD + 64 * h, it.start + it.q0(i));
                 }
-                mbar_arrive_expect_tx(bar, C::KT);
-                for (int h = 0; h < HD / 64; ++h)
-                    tma_load_2d((keys ? ring_k : ring_v) + at * C::KT + h * BN * 128, keys ? &tm_k : &tm_v, bar,
-                                kvh * HD + 64 * h, start + kb * BN);
-                (keys ? nk : nv) += 1;
+                for (int ik = 0, iv = 0; ok && iv < nb;) {
+                    const bool keys = ik < nb && ik - iv < 2;
+                    const int kb = keys ? ik : iv, g = keys ? nk : nv, ring = keys ? C::RK : C::RV, at = g % ring;
+                    if (g >= ring) ok = wait_warp(keys ? &k_empty[at] : &v_empty[at], (g / ring - 1) & 1);
+                    if (!ok) break;
+                    if (elect_one()) {
+                        uint64_t* bar = keys ? &k_full[at] : &v_full[at];
+                        if (!keys && kb >= scan0) {  // the scan waits for this one alone
+                            mbar_arrive(bar);
+                            bar = &v_in[at];
+                        }
+                        mbar_arrive_expect_tx(bar, C::KT);
+                        for (int h = 0; h < HD / 64; ++h)
+                            tma_load_2d((keys ? ring_k : ring_v) + at * C::KT + h * BN * 128, keys ? &tm_k : &tm_v, bar,
+                                        kvh * HD + 64 * h, it.start + kb * BN);
+                    }
+                    if (keys) ++ik, ++nk;
+                    else {
+                        if (kb >= scan0) ins ^= 1u << at;
+                        ++iv, ++nv;
+                    }
+                }
+                ++k;
             }
-            // All copies have landed before the block ends, also where a wait ran out.
-            for (int i = 0; i < NT; ++i)
-                if (i == 0 || nb1 > 0) mbar_wait_bounded(&q_full[i], 0, nullptr, p.timeout_ns);
-            for (int y = max(0, nk - C::RING); y < nk; ++y)
-                mbar_wait_bounded(&k_full[y % C::RING], (y / C::RING) & 1, nullptr, p.timeout_ns);
-            for (int y = max(0, nv - C::RING); y < nv; ++y)
-                mbar_wait_bounded(&v_full[y % C::RING], (y / C::RING) & 1, nullptr, p.timeout_ns);
-            for (int kb = scan0; kb < nv; ++kb) mbar_wait_bounded(&v_in[kb - scan0], 0, nullptr, p.timeout_ns);
+            // the answer is waited for in any case: it must not land in a block that has ended
+            const bool answered = __all_sync(0xffffffffu, mbar_wait_bounded(&answer_bar, asked & 1, nullptr, p.timeout_ns)) != 0;
+            ++asked;
+            if (!answered) *reinterpret_cast<volatile int*>(&dead) = 1, ok = false;
+            more = answered && next_block(&answer, x, y);
+            fence_proxy_async_smem();
+            __syncwarp();
         }
+        if (ok) announce(make_int4(0, 0, 0, 0));
+        // All copies have landed before the block ends, also where a wait ran out.
+        for (int i = max(0, k - 2); i < k; ++i) mbar_wait_bounded(&q_full[i & 1], (i >> 1) & 1, nullptr, p.timeout_ns);
+        for (int g = max(0, nk - C::RK); g < nk; ++g) mbar_wait_bounded(&k_full[g % C::RK], (g / C::RK) & 1, nullptr, p.timeout_ns);
+        for (int g = max(0, nv - C::RV); g < nv; ++g) mbar_wait_bounded(&v_full[g % C::RV], (g / C::RV) & 1, nullptr, p.timeout_ns);
+        for (int i = 0; i < C::RV; ++i)  // (an unused one passes: the phase before its first counts as done)
+            mbar_wait_bounded(&v_in[i], (ins >> i & 1) ^ 1, nullptr, p.timeout_ns);
     } else if (warp > NT * 4 && warp <= NT * 4 + NT) {
         // ---- products of tile i: the whole warp follows, one lane issues.  A warp per tile: one's
-        // products fill the time in which the other looks at its barriers.
+        // products fill the time in which the other looks at its barriers.  The scores run two blocks
+        // ahead of the products with V, over the ends of items.
         constexpr uint32_t fmt = std::is_same<T, __half>::value ? 0u : 1u;
         constexpr uint32_t idesc_s = idesc_f16(fmt, BM, BN, 0), idesc_o = idesc_f16(fmt, BM, HD, 1);
-        const int i = warp - NT * 4 - 1, mine = i == 0 ? nb0 : nb1;
-        auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
-        auto have_k = [&](int kb) { return wait_warp(&k_full[kb % C::RING], (kb / C::RING) & 1); };
-        auto scores = [&](int kb) {  // and K's buffer is free once they are done
-            if (kb < mine) {
-                const uint32_t q = smem_u32(base + i * C::QT), k = smem_u32(ring_k + kb % C::RING * C::KT);
-#pragma unroll
-                for (int s = 0; s < HD / 16; ++s)
-                    umma_f16(tmem + (2 * i + (kb & 1)) * BN, smem_desc_k128(q + (s >> 2) * QBOX) + 2 * (s & 3),
-                             smem_desc_k128(k + (s >> 2) * BN * 128) + 2 * (s & 3), idesc_s, s > 0);
-                umma_commit(&s_full[i][kb & 1]);
-            }
-            umma_commit(&k_empty[kb % C::RING]);
-        };
-        // the scores run two blocks ahead of the products with V
-        bool ok = mine == 0 || wait_warp(&q_full[i], 0);
-        for (int kb = 0; ok && kb < 2 && kb < nb; ++kb) {
-            ok = have_k(kb);
-            tc_fence_after();
-            if (ok && elect_one()) scores(kb);
-        }
-        for (int kb = 0; ok && kb < nb; ++kb) {
-            const int at = kb % C::RING;
-            ok = wait_warp(&v_full[at], (kb / C::RING) & 1) && (kb + 2 >= nb || have_k(kb + 2)) &&
-                 (kb < scan0 || (wait_warp(&v_in[kb - scan0], 0) && wait_warp(&v_ok[kb - scan0], 0))) &&
-                 (kb >= mine || wait_warp(&p_full[i][kb & 1], (kb >> 1) & 1));
-            tc_fence_after();
-            if (ok && elect_one()) {
-                if (kb < mine) {
-                    const uint32_t v = smem_u32(ring_v + at * C::KT);
-#pragma unroll
-                    for (int s = 0; s < BN / 16; ++s)
-                        umma_f16_tmem_a(tmem + C::O_COL + i * HD, tmem + (2 * i + (kb & 1)) * BN + s * 8,
-                                        smem_desc_mn128(v + s * 2048, BN * 128, 1024), idesc_o, kb > 0 || s > 0);
-                    umma_commit(kb + 1 < mine ? &o_done[i] : &o_full[i]);
+        const int i = warp - NT * 4 - 1;
+        bool ok = true, end = false;
+        PromptItem ahead = it;
+        int a_item = 0, a_kb = 0, a_nb = 0, a_mine = 0, a_x = 0, a_g = 0;  // the scores: item, block, K block and own block in all
+        auto scores = [&]() {
+            if (end) return;
+            if (a_kb == a_nb) {
+                ok = item_there(a_item);
+                if (!ok) return;
+                read_item(a_item, ahead, false);
+                if (ahead.n == 0) {
+                    end = true;
+                    return;
                 }
-                umma_commit(&v_empty[at]);
-                if (kb + 2 < nb) scores(kb + 2);  // over the scores of block kb: these products come first
+                ok = wait_warp(&q_full[a_item & 1], (a_item >> 1) & 1);
+                if (!ok) return;
+                a_nb = ahead.all_blocks<NT>(), a_mine = ahead.blocks(i), a_kb = 0;
+                ++a_item;
+            }
+            const int at = a_x % C::RK;
+            ok = wait_warp(&k_full[at], (a_x / C::RK) & 1);
+            if (!ok) return;
+            tc_fence_after();
+            if (elect_one()) {
+                if (a_kb < a_mine) {
+                    const uint32_t q = smem_u32(q_tile(a_item - 1, i)), k = smem_u32(ring_k + at * C::KT);
+#pragma unroll
+                    for (int s = 0; s < HD / 16; ++s)
+                        umma_f16(tmem + (2 * i + (a_g & 1)) * BN, smem_desc_k128(q + (s >> 2) * QBOX) + 2 * (s & 3),
+                                 smem_desc_k128(k + (s >> 2) * BN * 128) + 2 * (s & 3), idesc_s, s > 0);
+                    umma_commit(&s_full[i][a_g & 1]);
+                }
+                umma_commit(&k_empty[at]);  // K's buffer is free once they are done
+            }
+            __syncwarp();
+            if (a_kb < a_mine) ++a_g;
+            ++a_kb, ++a_x;
+        };
+        scores();
+        if (ok) scores();
+        uint32_t ins = 0, scans = 0;  // parities of the next uses of v_in, v_ok
+        for (int k = 0, x = 0, g = 0; ok; ++k) {
+            ok = item_there(k);
+            if (!ok) break;
+            read_item(k, it, true);
+            if (it.n == 0) break;
+            const int nb = it.all_blocks<NT>(), mine = it.blocks(i), scan0 = it.scan0();
+            for (int kb = 0; ok && kb < nb; ++kb, ++x) {
+                const int at = x % C::RV;
+                ok = wait_warp(&v_full[at], (x / C::RV) & 1);
+                if (ok && kb >= scan0) {
+                    const int j = kb - scan0;
+                    ok = wait_warp(&v_in[at], ins >> at & 1) && wait_warp(&v_ok[j], scans >> j & 1);
+                    ins ^= 1u << at, scans ^= 1u << j;
+                }
+                if (ok && kb < mine) ok = wait_warp(&p_full[i][g & 1], (g >> 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    if (kb < mine) {
+                        const uint32_t v = smem_u32(ring_v + at * C::KT);
+#pragma unroll
+                        for (int s = 0; s < BN / 16; ++s)
+                            umma_f16_tmem_a(tmem + C::O_COL + i * HD, tmem + (2 * i + (g & 1)) * BN + s * 8,
+                                            smem_desc_mn128(v + s * 2048, BN * 128, 1024), idesc_o, kb > 0 || s > 0);
+                        umma_commit(kb + 1 < mine ? &o_done[i] : &o_full[i]);
+                    }
+                    umma_commit(&v_empty[at]);
+                }
+                __syncwarp();
+                if (kb < mine) ++g;
+                scores();  // over the scores of this block: its products come first
             }
         }
         if (elect_one()) umma_commit(&drain[i]);  // all products are done before the block ends
@@ -244,168 +431,202 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         // ---- scan of V
         constexpr uint32_t INF = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
         const int me = tid - (NT * 4 + NT + 1) * 32;
-        for (int kb = scan0; kb < nb; ++kb) {
-            if (!wait(&v_in[kb - scan0], 0)) break;
-            uint8_t* v = ring_v + kb % C::RING * C::KT;
-            for (int r = me; r < BN; r += C::SCAN) {
-                const int t = kb * BN + r;
-                uint32_t most = 0;
-                if (t < n) {
+        uint32_t ins = 0;
+        bool ok = true;
+        for (int k = 0, x = 0;; ++k) {
+            // (its warps leave together: they meet at barriers)
+            if (!scan_sync<C::SCAN>(ok && item_there(k))) break;
+            read_item(k, it, true);
+            if (it.n == 0) break;
+            const int nb = it.all_blocks<NT>(), scan0 = it.scan0();
+            // what was noted for the item before is read once its outputs are stored
+            if (k > 0) ok = wait_warp(&q_free[(k - 1) & 1], ((k - 1) >> 1) & 1);
+            if (!scan_sync<C::SCAN>(ok)) break;
+            if (*reinterpret_cast<volatile int*>(&odd) == k)
+                for (int d = me; d < HD; d += C::SCAN) first[d] = NONE_BAD;
+            scan_sync<C::SCAN>(true);
+            for (int kb = scan0; kb < nb; ++kb) {
+                const int at = (x + kb) % C::RV;
+                ok = wait_warp(&v_in[at], ins >> at & 1);
+                ins ^= 1u << at;
+                if (!ok) break;
+                uint8_t* v = ring_v + at * C::KT;
+                for (int r = me; r < BN; r += C::SCAN) {
+                    const int t = kb * BN + r;
+                    uint32_t most = 0;
+                    if (t < it.n) {
 #pragma unroll
-                    for (int ch = 0; ch < HD / 8; ++ch) {
-                        const uint4 w = *reinterpret_cast<const uint4*>(v + (ch >> 3) * BN * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
-                        most = __vmaxu2(__vmaxu2(__vmaxu2(most, w.x & 0x7fff7fffu), __vmaxu2(w.y & 0x7fff7fffu, w.z & 0x7fff7fffu)),
-                                        w.w & 0x7fff7fffu);
-                    }
-                    if ((most & 0xffffu) < INF && (most >> 16) < INF) continue;
-                    for (int d = 0; d < HD; ++d) {
-                        uint16_t* e = reinterpret_cast<uint16_t*>(v + (d >> 6) * BN * 128 + r * 128 +
-                                                                  (((d >> 3 & 7) ^ (r & 7)) << 4)) + (d & 7);
-                        const uint32_t w = *e;
-                        if ((w & 0x7fffu) < INF) continue;
-                        atomicMin(&first[(w & 0x7fffu) > INF ? 2 : w >> 15][d], t);
-                        *e = 0;
-                    }
-                    odd = 1;
-                } else {
+                        for (int ch = 0; ch < HD / 8; ++ch) {
+                            const uint4 w = *reinterpret_cast<const uint4*>(v + (ch >> 3) * BN * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+                            most = __vmaxu2(__vmaxu2(__vmaxu2(most, w.x & 0x7fff7fffu), __vmaxu2(w.y & 0x7fff7fffu, w.z & 0x7fff7fffu)),
+                                            w.w & 0x7fff7fffu);
+                        }
+                        if ((most & 0xffffu) < INF && (most >> 16) < INF) continue;
+                        for (int d = 0; d < HD; ++d) {
+                            uint16_t* e = reinterpret_cast<uint16_t*>(v + (d >> 6) * BN * 128 + r * 128 +
+                                                                      (((d >> 3 & 7) ^ (r & 7)) << 4)) + (d & 7);
+                            const uint32_t w = *e;
+                            if ((w & 0x7fffu) < INF) continue;
+                            note_bad(&first[d], (w & 0x7fffu) > INF ? 2 : w >> 15, t - scan0 * BN);
+                            *e = 0;
+                        }
+                        odd = k + 1;
+                    } else {
 #pragma unroll
-                    for (int ch = 0; ch < HD / 8; ++ch)
-                        *reinterpret_cast<uint4*>(v + (ch >> 3) * BN * 128 + r * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        for (int ch = 0; ch < HD / 8; ++ch)
+                            *reinterpret_cast<uint4*>(v + (ch >> 3) * BN * 128 + r * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
                 }
+                fence_proxy_async_smem();
+                mbar_arrive(&v_ok[kb - scan0]);
             }
-            fence_proxy_async_smem();
-            mbar_arrive(&v_ok[kb - scan0]);
+            x += nb;
         }
     } else {
         // ---- softmax of tile i, one query per thread
-        const int i = NT == 2 ? warp >> 2 : 0, row = tid & 127, q0 = q0_of(i), s = q0 + row;
-        const int mine = i == 0 ? nb0 : nb1;
+        const int i = NT == 2 ? warp >> 2 : 0, row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t S0 = tmem + lanes + 2 * i * BN, O = tmem + lanes + C::O_COL + i * HD;
-        float m = -INFINITY, mc = 0.0f;  // the maximum that the exponentials refer to, and times c (0 for -infinity)
-        uint64_t sum[4] = {0, 0, 0, 0};  // pairs of partial sums (+0.0)
-        // TMEM is read and written by whole warps: their lanes give up together
-        auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
-        bool ok = true;
-        for (int kb = 0; kb < mine; ++kb) {
-            const uint32_t S = S0 + (kb & 1) * BN;
-            ok = wait_warp(&s_full[i][kb & 1], (kb >> 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            uint32_t x[BN];
-            tmem_ld_x32(S, x);
-            tmem_ld_x32(S + 32, x + 32);
-            tmem_wait_ld_regs(x);
-            tmem_wait_ld_regs(x + 32);
-            if (kb >= q0 / BN) {
-                const int see = s - kb * BN;  // keys up to here
-#pragma unroll
-                for (int e = 0; e < BN; ++e)
-                    if (e > see) x[e] = 0xff800000u;
-            }
-            const float mx = max_of<BN>(x);
-            if (kb == 0) {
-                m = mx;
-                mc = m == -INFINITY ? 0.0f : m * a.c;
-            } else if (__any_sync(0xffffffffu, (mx - m) * a.c > GROW)) {
-                // O is at rest once the products of block kb - 1 are done; those of kb - 2 were before S,
-                // those of kb wait for this thread: the phase is the barrier's current or last one
-                ok = wait_warp(&o_done[i], (kb - 1) & 1);
+        uint32_t scans = 0;
+        // g: blocks of this tile so far; done: products with V that were not an item's last; own: items with queries
+        for (int k = 0, g = 0, done = 0, own = 0;; ++k) {
+            // the tile's warps take an item, or leave, together: they meet at a barrier below
+            if (!tile_sync(1 + i, item_there(k))) break;
+            read_item(k, it, true);
+            if (it.n == 0) break;
+            const int q0 = it.q0(i), s = q0 + row, mine = it.blocks(i), nb = it.all_blocks<NT>(), scan0 = it.scan0();
+            float m = -INFINITY, mc = 0.0f;  // the maximum that the exponentials refer to, and times c (0 for -infinity)
+            uint64_t sum[4] = {0, 0, 0, 0};  // pairs of partial sums (+0.0)
+            bool ok = true;
+            for (int kb = 0; kb < mine; ++kb, ++g) {
+                const uint32_t S = S0 + (g & 1) * BN;
+                ok = wait_warp(&s_full[i][g & 1], (g >> 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
-                float by = 1.0f;
-                if ((mx - m) * a.c > GROW) {
-                    by = m == -INFINITY ? 0.0f : exp2_fast(mc - mx * a.c);
-                    m = mx, mc = mx * a.c;
-                }
+                uint32_t x[BN];
+                tmem_ld_x32(S, x);
+                tmem_ld_x32(S + 32, x + 32);
+                tmem_wait_ld_regs(x);
+                tmem_wait_ld_regs(x + 32);
+                if (kb >= q0 / BN) {
+                    const int see = s - kb * BN;  // keys up to here
 #pragma unroll
-                for (int y = 0; y < 4; ++y) sum[y] = mul2(sum[y], two(by, by));
+                    for (int e = 0; e < BN; ++e)
+                        if (e > see) x[e] = 0xff800000u;
+                }
+                const float mx = max_of<BN>(x);
+                if (kb == 0) {
+                    m = mx;
+                    mc = m == -INFINITY ? 0.0f : m * a.c;
+                } else if (__any_sync(0xffffffffu, (mx - m) * a.c > GROW)) {
+                    // O is at rest once the products of block kb - 1 are done; those of kb - 2 were before S,
+                    // those of kb wait for this thread: the phase is the barrier's current or last one
+                    ok = wait_warp(&o_done[i], (done + kb - 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    float by = 1.0f;
+                    if ((mx - m) * a.c > GROW) {
+                        by = m == -INFINITY ? 0.0f : exp2_fast(mc - mx * a.c);
+                        m = mx, mc = mx * a.c;
+                    }
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) sum[y] = mul2(sum[y], two(by, by));
+#pragma unroll 1
+                    for (int h = 0; h < HD / 32; ++h) {
+                        uint32_t o[32];
+                        tmem_ld_x32(O + 32 * h, o);
+                        tmem_wait_ld_regs(o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
+                        tmem_st_x32(O + 32 * h, o);
+                    }
+                }
+                const uint64_t c2 = two(a.c, a.c), m2 = two(-mc, -mc);
+#pragma unroll
+                for (int h = 0; h < BN / 32; ++h) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const uint32_t* y = x + 32 * h + 2 * e;
+                        const float2 z = one_by_one(fma2(two(__uint_as_float(y[0]), __uint_as_float(y[1])), c2, m2));
+                        const float e0 = exp2_fast(z.x), e1 = exp2_fast(z.y);
+                        sum[e & 3] = add2(sum[e & 3], two(e0, e1));
+                        w[e] = pack2<T>(e0, e1);
+                    }
+                    tmem_st_x16(S + 16 * h, w);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&p_full[i][g & 1]);
+            }
+            uint8_t* out = q_tile(k, i);
+            // a tile without queries keeps pace: it must not free the next Q in the place of this one
+            if (mine == 0) ok = wait_warp(&q_full[k & 1], (k >> 1) & 1);
+            if (mine > 0 && ok) ok = wait_warp(&o_full[i], own & 1);
+            // values that are not finite, as noted for the blocks that this tile reads
+            for (int kb = scan0; ok && kb < mine; ++kb) ok = wait_warp(&v_ok[kb - scan0], scans >> (kb - scan0) & 1);
+            for (int kb = scan0; kb < nb; ++kb) scans ^= 1u << (kb - scan0);
+            if (mine > 0 && ok) {
+                tc_fence_after();
+                const float2 l2 = one_by_one(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+                const float l = l2.x + l2.y, inv = 1.0f / l;
+                const bool fix = *reinterpret_cast<volatile int*>(&odd) == k + 1;
+                // O / l, rounded, over the Q tile (no product reads it any more), 128-byte swizzle
 #pragma unroll 1
                 for (int h = 0; h < HD / 32; ++h) {
                     uint32_t o[32];
                     tmem_ld_x32(O + 32 * h, o);
                     tmem_wait_ld_regs(o);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
-                    tmem_st_x32(O + 32 * h, o);
-                }
-            }
-            const uint64_t c2 = two(a.c, a.c), m2 = two(-mc, -mc);
-#pragma unroll
-            for (int h = 0; h < BN / 32; ++h) {
-                uint32_t w[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const uint32_t* y = x + 32 * h + 2 * e;
-                    const float2 z = one_by_one(fma2(two(__uint_as_float(y[0]), __uint_as_float(y[1])), c2, m2));
-                    const float e0 = exp2_fast(z.x), e1 = exp2_fast(z.y);
-                    sum[e & 3] = add2(sum[e & 3], two(e0, e1));
-                    w[e] = pack2<T>(e0, e1);
-                }
-                tmem_st_x16(S + 16 * h, w);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(&p_full[i][kb & 1]);
-        }
-        if (mine > 0 && ok) ok = wait_warp(&o_full[i], 0);
-        // values that are not finite, as noted for the blocks that this tile reads
-        for (int kb = scan0; ok && kb < mine; ++kb) ok = wait_warp(&v_ok[kb - scan0], 0);
-        if (mine > 0 && ok) {
-            tc_fence_after();
-            const float2 l2 = one_by_one(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
-            const float l = l2.x + l2.y, inv = 1.0f / l;
-            const bool fix = *reinterpret_cast<volatile int*>(&odd) != 0;
-            // O / l, rounded, over the Q tile (no product reads it any more), 128-byte swizzle
-            uint8_t* out = base + i * C::QT;
-#pragma unroll 1
-            for (int h = 0; h < HD / 32; ++h) {
-                uint32_t o[32];
-                tmem_ld_x32(O + 32 * h, o);
-                tmem_wait_ld_regs(o);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    float f = __uint_as_float(o[e]) * inv;
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
                     if (fix) {
-                        if (s >= first[0][32 * h + e]) f += INFINITY;
-                        if (s >= first[1][32 * h + e]) f -= INFINITY;
-                        if (s >= first[2][32 * h + e]) f = NAN;
-                    }
-                    o[e] = __float_as_uint(f);
-                }
+                        const int at = s - scan0 * BN;
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    uint4 w;
-                    w.x = pack2<T>(__uint_as_float(o[8 * g]), __uint_as_float(o[8 * g + 1]));
-                    w.y = pack2<T>(__uint_as_float(o[8 * g + 2]), __uint_as_float(o[8 * g + 3]));
-                    w.z = pack2<T>(__uint_as_float(o[8 * g + 4]), __uint_as_float(o[8 * g + 5]));
-                    w.w = pack2<T>(__uint_as_float(o[8 * g + 6]), __uint_as_float(o[8 * g + 7]));
-                    const int ch = (h & 1) * 4 + g;
-                    *reinterpret_cast<uint4*>(out + (h >> 1) * QBOX + row * 128 + ((ch ^ (row & 7)) << 4)) = w;
+                        for (int e = 0; e < 32; ++e) {
+                            const uint32_t w = *reinterpret_cast<const volatile uint32_t*>(&first[32 * h + e]);
+                            float f = __uint_as_float(o[e]);
+                            if (at >= (int)(w & 511u)) f += INFINITY;
+                            if (at >= (int)(w >> 9 & 511u)) f -= INFINITY;
+                            if (at >= (int)(w >> 18)) f = NAN;
+                            o[e] = __float_as_uint(f);
+                        }
+                    }
+#pragma unroll
+                    for (int g4 = 0; g4 < 4; ++g4) {
+                        uint4 w;
+                        w.x = pack2<T>(__uint_as_float(o[8 * g4]), __uint_as_float(o[8 * g4 + 1]));
+                        w.y = pack2<T>(__uint_as_float(o[8 * g4 + 2]), __uint_as_float(o[8 * g4 + 3]));
+                        w.z = pack2<T>(__uint_as_float(o[8 * g4 + 4]), __uint_as_float(o[8 * g4 + 5]));
+                        w.w = pack2<T>(__uint_as_float(o[8 * g4 + 6]), __uint_as_float(o[8 * g4 + 7]));
+                        const int ch = (h & 1) * 4 + g4;
+                        *reinterpret_cast<uint4*>(out + (h >> 1) * QBOX + row * 128 + ((ch ^ (row & 7)) << 4)) = w;
+                    }
                 }
+                tc_fence_before();  // the next item's products write over O
+                if (s < it.n && p.lse != nullptr) p.lse[(int64_t)it.head(i) * p.rows + it.start + s] = (mc + log2f(l)) * LN2;
+                fence_proxy_async_smem();
             }
-            if (s < n && p.lse != nullptr) p.lse[(int64_t)head_of(i) * p.rows + start + s] = (mc + log2f(l)) * LN2;
-            fence_proxy_async_smem();
-        }
-        // (all threads of the tile agree on `mine`; a wait that ran out lets none of them store)
-        wg_sync(1 + i);
-        if (mine > 0 && *reinterpret_cast<volatile int*>(&dead) == 0) {
-            uint8_t* out = base + i * C::QT;
-            const int rows = min(BM, n - q0);
-            if (rows == BM) {
-                if (row == 0) {
-                    for (int h = 0; h < HD / 64; ++h) tma_store_2d(&tm_o, out + h * QBOX, head_of(i) * HD + 64 * h, start + q0);
-                    bulk_commit();
-                    bulk_wait_read<0>();
+            if (!tile_sync(1 + i, ok)) break;
+            if (mine > 0) {
+                const int rows = min(BM, it.n - q0);
+                if (rows == BM) {
+                    if (row == 0) {
+                        for (int h = 0; h < HD / 64; ++h) tma_store_2d(&tm_o, out + h * QBOX, it.head(i) * HD + 64 * h, it.start + q0);
+                        bulk_commit();
+                        bulk_wait_read<0>();
+                    }
+                } else {
+                    constexpr int PER = HD / 8;  // 16-byte pieces of a row
+                    for (int y = row; y < rows * PER; y += 128) {
+                        const int r = y / PER, ch = y % PER;
+                        const uint4 w = *reinterpret_cast<const uint4*>(out + (ch >> 3) * QBOX + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+                        *reinterpret_cast<uint4*>(static_cast<T*>(p.o) + (int64_t)(it.start + q0 + r) * p.ld_o + (int64_t)it.head(i) * HD + ch * 8) = w;
+                    }
                 }
-            } else {
-                constexpr int PER = HD / 8;  // 16-byte pieces of a row
-                for (int y = row; y < rows * PER; y += 128) {
-                    const int r = y / PER, ch = y % PER;
-                    const uint4 w = *reinterpret_cast<const uint4*>(out + (ch >> 3) * QBOX + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
-                    *reinterpret_cast<uint4*>(static_cast<T*>(p.o) + (int64_t)(start + q0 + r) * p.ld_o + (int64_t)head_of(i) * HD + ch * 8) = w;
-                }
+                done += mine - 1, ++own;
             }
+            fence_proxy_async_smem();  // what was read here is loaded over next
+            mbar_arrive(&q_free[k & 1]);
         }
     }
     __syncwarp();
@@ -436,13 +657,15 @@ cudaError_t rows_map(CUtensorMap* m, int dtype, const void* ptr, int64_t cols, i
 template <typename T, int HD, int NT>
 static cudaError_t prompt_tc(const PromptArgs& p, cudaStream_t st) {
     using C = TCfg<HD, NT>;
+    constexpr int SMEM = C::TILES + (int)sizeof(Aux<HD, NT>);
+    static_assert(C::CTAS * (SMEM + 1024) <= 228 * 1024, "the blocks of an SM share its memory");
     CUtensorMap q, k, v, o;
     const int64_t wq = (int64_t)p.n_heads * HD, wk = (int64_t)p.n_kv * HD;
     cudaError_t e = rows_map(&q, p.dtype, p.q, wq, p.rows, p.ld_q, BM);
     if (e == cudaSuccess) e = rows_map(&k, p.dtype, p.k, wk, p.rows, p.ld_k, BN);
     if (e == cudaSuccess) e = rows_map(&v, p.dtype, p.v, wk, p.rows, p.ld_v, BN);
     if (e == cudaSuccess) e = rows_map(&o, p.dtype, p.o, wq, p.rows, p.ld_o, BM);
-    if (e == cudaSuccess) e = prepare_smem((const void*)prompt_tc_kernel<T, HD, NT>, C::SMEM);
+    if (e == cudaSuccess) e = prepare_smem((const void*)prompt_tc_kernel<T, HD, NT>, SMEM);
     if (e != cudaSuccess) return e;
     PromptTcArgs a;
     a.p = p;
@@ -452,7 +675,7 @@ static cudaError_t prompt_tc(const PromptArgs& p, cudaStream_t st) {
     const int most = p.rows / tile + (p.batch < p.rows ? p.batch : p.rows);
     a.head_steps = a.pair_heads ? p.n_heads / 2 : p.n_heads;
     const dim3 grid(most, a.head_steps);
-    prompt_tc_kernel<T, HD, NT><<<grid, C::THREADS, C::SMEM, st>>>(q, k, v, o, a);
+    prompt_tc_kernel<T, HD, NT><<<grid, C::THREADS, SMEM, st>>>(q, k, v, o, a);
     return cudaGetLastError();
 }
 
