@@ -40,10 +40,11 @@ template <int HD, int NT>
 struct TCfg {
     static constexpr int QT = HD / 64 * QBOX;                // bytes of a Q tile
     static constexpr int KT = HD * BN * 2;                   // bytes of a K or V block
-    // buffers of K and of V; the Q tiles have two
-    static constexpr int RK = NT == 2 ? (HD == 128 ? 3 : 6) : (HD == 128 ? 2 : 4);
-    static constexpr int RV = NT == 2 ? (HD == 128 ? 3 : 6) : (HD == 128 ? 1 : 4);
-    static constexpr int TILES = 2 * NT * QT + (RK + RV) * KT;
+    // buffers of K and of V; 4 KB for each softmax warp's outputs
+    static constexpr int RK = NT == 2 ? (HD == 128 ? 4 : 8) : (HD == 128 ? 2 : 4);
+    static constexpr int RV = RK;
+    static constexpr int OUT = 32 * 128;
+    static constexpr int TILES = NT * QT + (RK + RV) * KT + NT * 4 * OUT;
     static constexpr int THREADS = NT * 128 + 128;
     static constexpr int SCAN = NT == 2 ? 32 : 64;           // threads that scan V
     static constexpr int O_COL = NT * 2 * BN;                // S takes two buffers per tile
@@ -159,7 +160,7 @@ struct PromptTcArgs {
 template <int HD, int NT>
 struct Aux {
     using C = TCfg<HD, NT>;
-    uint64_t q_full[2], q_free[2], o_done[NT], o_full[NT], drain[NT], s_full[NT][2], p_full[NT][2];
+    uint64_t q_full, q_empty, out_done, o_done[NT], o_full[NT], drain[NT], s_full[NT][2], p_full[NT][2];
     uint64_t k_full[C::RK], k_empty[C::RK], v_full[C::RV], v_empty[C::RV];
     uint64_t v_in[C::RV];     // a block that is scanned has landed in this buffer
     uint64_t v_ok[C::SCANS];  // an item's first, second, ... such block is scanned
@@ -187,13 +188,13 @@ struct PromptItem {
 template <typename T, int HD, int NT>
 __global__ void __launch_bounds__(TCfg<HD, NT>::THREADS, TCfg<HD, NT>::CTAS)
 prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
-                 const PromptTcArgs a) {
+                 const __grid_constant__ CUtensorMap tm_v, const PromptTcArgs a) {
     using C = TCfg<HD, NT>;
     extern __shared__ __align__(1024) uint8_t base[];  // the tiles, swizzled in units of 1024 bytes, then Aux
     Aux<HD, NT>& aux = *reinterpret_cast<Aux<HD, NT>*>(base + C::TILES);
     auto& q_full = aux.q_full;
-    auto& q_free = aux.q_free;
+    auto& q_empty = aux.q_empty;
+    auto& out_done = aux.out_done;
     auto& o_done = aux.o_done;
     auto& o_full = aux.o_full;
     auto& drain = aux.drain;
@@ -219,12 +220,11 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int tile_rows = NT == 2 && !a.pair_heads ? 2 * BM : BM;
 
-    uint8_t* ring_k = base + 2 * NT * C::QT;
+    uint8_t* ring_k = base + NT * C::QT;
     uint8_t* ring_v = ring_k + C::RK * C::KT;
-    auto q_tile = [&](int k, int i) { return base + ((k & 1) * NT + i) * C::QT; };  // of item k
     for (int i = tid; i < HD; i += C::THREADS) first[i] = NONE_BAD;
     if (tid == 0) {
-        for (int i = 0; i < 2; ++i) mbar_init(&q_full[i], 1), mbar_init(&q_free[i], NT * 128);
+        mbar_init(&q_full, 1), mbar_init(&q_empty, NT), mbar_init(&out_done, NT * 128);
         for (int i = 0; i < NT; ++i) {
             mbar_init(&o_done[i], 1), mbar_init(&o_full[i], 1), mbar_init(&drain[i], 1);
             for (int y = 0; y < 2; ++y) mbar_init(&s_full[i][y], 1), mbar_init(&p_full[i][y], 128);
@@ -298,13 +298,13 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 it.head0 = (int)(lin % a.head_steps) * (a.pair_heads ? 2 : 1);
                 announce(make_int4(it.start, it.n, it.blk, it.head0));
                 const int kvh = it.head0 / (p.n_heads / p.n_kv), nb = it.all_blocks<NT>(), scan0 = it.scan0();
-                if (ok && k >= 2) ok = wait_warp(&q_free[k & 1], ((k >> 1) - 1) & 1);
+                if (ok && k >= 1) ok = wait_warp(&q_empty, (k - 1) & 1);
                 if (ok && elect_one()) {
                     const int tiles = NT == 2 && it.blocks(NT - 1) > 0 ? NT : 1;
-                    mbar_arrive_expect_tx(&q_full[k & 1], tiles * C::QT);
+                    mbar_arrive_expect_tx(&q_full, tiles * C::QT);
                     for (int i = 0; i < tiles; ++i)
                         for (int h = 0; h < HD / 64; ++h)
-                            tma_load_2d(q_tile(k, i) + h * QBOX, &tm_q, &q_full[k & 1], it.head(i) * HD + 64 * h, it.start + it.q0(i));
+                            tma_load_2d(base + i * C::QT + h * QBOX, &tm_q, &q_full, it.head(i) * HD + 64 * h, it.start + it.q0(i));
                 }
                 for (int ik = 0, iv = 0; ok && iv < nb;) {
                     const bool keys = ik < nb && ik - iv < 2;
@@ -340,89 +340,98 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
         if (ok) announce(make_int4(0, 0, 0, 0));
         // All copies have landed before the block ends, also where a wait ran out.
-        for (int i = max(0, k - 2); i < k; ++i) mbar_wait_bounded(&q_full[i & 1], (i >> 1) & 1, nullptr, p.timeout_ns);
+        if (k > 0) mbar_wait_bounded(&q_full, (k - 1) & 1, nullptr, p.timeout_ns);
         for (int g = max(0, nk - C::RK); g < nk; ++g) mbar_wait_bounded(&k_full[g % C::RK], (g / C::RK) & 1, nullptr, p.timeout_ns);
         for (int g = max(0, nv - C::RV); g < nv; ++g) mbar_wait_bounded(&v_full[g % C::RV], (g / C::RV) & 1, nullptr, p.timeout_ns);
         for (int i = 0; i < C::RV; ++i)  // (an unused one passes: the phase before its first counts as done)
             mbar_wait_bounded(&v_in[i], (ins >> i & 1) ^ 1, nullptr, p.timeout_ns);
     } else if (warp > NT * 4 && warp <= NT * 4 + NT) {
         // ---- products of tile i: the whole warp follows, one lane issues.  A warp per tile: one's
-        // products fill the time in which the other looks at its barriers.  The scores run two blocks
-        // ahead of the products with V, over the ends of items.
+        // products fill the time in which the other looks at its barriers.  The scores run up to two blocks
+        // ahead of the products with V, over the ends of items; whichever of the two can go on does (the
+        // next item's Q may still be on its way when the last products of this one are due).
         constexpr uint32_t fmt = std::is_same<T, __half>::value ? 0u : 1u;
         constexpr uint32_t idesc_s = idesc_f16(fmt, BM, BN, 0), idesc_o = idesc_f16(fmt, BM, HD, 1);
         const int i = warp - NT * 4 - 1;
-        bool ok = true, end = false;
+        auto there = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_wait(bar, parity)) != 0; };
+        // the scores: item, its block, K block and own block in all; has: the item is read
         PromptItem ahead = it;
-        int a_item = 0, a_kb = 0, a_nb = 0, a_mine = 0, a_x = 0, a_g = 0;  // the scores: item, block, K block and own block in all
-        auto scores = [&]() {
-            if (end) return;
-            if (a_kb == a_nb) {
-                ok = item_there(a_item);
-                if (!ok) return;
-                read_item(a_item, ahead, false);
-                if (ahead.n == 0) {
-                    end = true;
-                    return;
-                }
-                ok = wait_warp(&q_full[a_item & 1], (a_item >> 1) & 1);
-                if (!ok) return;
-                a_nb = ahead.all_blocks<NT>(), a_mine = ahead.blocks(i), a_kb = 0;
-                ++a_item;
-            }
-            const int at = a_x % C::RK;
-            ok = wait_warp(&k_full[at], (a_x / C::RK) & 1);
-            if (!ok) return;
-            tc_fence_after();
-            if (elect_one()) {
-                if (a_kb < a_mine) {
-                    const uint32_t q = smem_u32(q_tile(a_item - 1, i)), k = smem_u32(ring_k + at * C::KT);
-#pragma unroll
-                    for (int s = 0; s < HD / 16; ++s)
-                        umma_f16(tmem + (2 * i + (a_g & 1)) * BN, smem_desc_k128(q + (s >> 2) * QBOX) + 2 * (s & 3),
-                                 smem_desc_k128(k + (s >> 2) * BN * 128) + 2 * (s & 3), idesc_s, s > 0);
-                    umma_commit(&s_full[i][a_g & 1]);
-                }
-                umma_commit(&k_empty[at]);  // K's buffer is free once they are done
-            }
-            __syncwarp();
-            if (a_kb < a_mine) ++a_g;
-            ++a_kb, ++a_x;
-        };
-        scores();
-        if (ok) scores();
+        int a_item = 0, a_kb = 0, a_nb = 0, a_mine = 0, a_x = 0, a_g = 0;
+        bool end = false, has = false;
+        // the products with V: the same
+        int k = 0, kb = 0, nb = 0, mine = 0, scan0 = 0, x = 0, g = 0;
         uint32_t ins = 0, scans = 0;  // parities of the next uses of v_in, v_ok
-        for (int k = 0, x = 0, g = 0; ok; ++k) {
-            ok = item_there(k);
-            if (!ok) break;
-            read_item(k, it, true);
-            if (it.n == 0) break;
-            const int nb = it.all_blocks<NT>(), mine = it.blocks(i), scan0 = it.scan0();
-            for (int kb = 0; ok && kb < nb; ++kb, ++x) {
-                const int at = x % C::RV;
-                ok = wait_warp(&v_full[at], (x / C::RV) & 1);
-                if (ok && kb >= scan0) {
-                    const int j = kb - scan0;
-                    ok = wait_warp(&v_in[at], ins >> at & 1) && wait_warp(&v_ok[j], scans >> j & 1);
-                    ins ^= 1u << at, scans ^= 1u << j;
-                }
-                if (ok && kb < mine) ok = wait_warp(&p_full[i][g & 1], (g >> 1) & 1);
-                if (!ok) break;
+        uint64_t since = 0;
+        for (uint32_t idle = 0;;) {
+            bool moved = false;
+            if (!end && !has && there(&item_full[a_item % ITEMS], (a_item / ITEMS) & 1)) {
+                read_item(a_item, ahead, false);
+                end = ahead.n == 0;
+                has = !end;
+                a_nb = ahead.all_blocks<NT>(), a_mine = ahead.blocks(i), a_kb = 0;
+            }
+            const int ka = a_x % C::RK;
+            // (over the scores of the block two before: its products come first)
+            if (has && a_x - x < 2 && (a_kb > 0 || there(&q_full, a_item & 1)) && there(&k_full[ka], (a_x / C::RK) & 1)) {
                 tc_fence_after();
                 if (elect_one()) {
-                    if (kb < mine) {
-                        const uint32_t v = smem_u32(ring_v + at * C::KT);
+                    if (a_kb < a_mine) {
+                        const uint32_t q = smem_u32(base + i * C::QT), kk = smem_u32(ring_k + ka * C::KT);
 #pragma unroll
-                        for (int s = 0; s < BN / 16; ++s)
-                            umma_f16_tmem_a(tmem + C::O_COL + i * HD, tmem + (2 * i + (g & 1)) * BN + s * 8,
-                                            smem_desc_mn128(v + s * 2048, BN * 128, 1024), idesc_o, kb > 0 || s > 0);
-                        umma_commit(kb + 1 < mine ? &o_done[i] : &o_full[i]);
+                        for (int s = 0; s < HD / 16; ++s)
+                            umma_f16(tmem + (2 * i + (a_g & 1)) * BN, smem_desc_k128(q + (s >> 2) * QBOX) + 2 * (s & 3),
+                                     smem_desc_k128(kk + (s >> 2) * BN * 128) + 2 * (s & 3), idesc_s, s > 0);
+                        umma_commit(&s_full[i][a_g & 1]);
                     }
-                    umma_commit(&v_empty[at]);
+                    umma_commit(&k_empty[ka]);  // K's buffer is free once they are done, and after an item's last ones Q's
+                    if (a_kb + 1 == a_nb) umma_commit(&q_empty);
                 }
                 __syncwarp();
-                if (kb < mine) ++g;
-                scores();  // over the scores of this block: its products come first
+                if (a_kb < a_mine) ++a_g;
+                ++a_x;
+                if (++a_kb == a_nb) has = false, ++a_item;
+                moved = true;
+            }
+            if (x < a_x) {  // its scores are under way, so its item was announced
+                if (kb == nb) {
+                    read_item(k, it, true);
+                    nb = it.all_blocks<NT>(), mine = it.blocks(i), scan0 = it.scan0(), kb = 0, ++k;
+                }
+                const int at = x % C::RV, j = kb - scan0;
+                if ((kb >= mine || there(&p_full[i][g & 1], (g >> 1) & 1)) && there(&v_full[at], (x / C::RV) & 1) &&
+                    (j < 0 || (there(&v_in[at], ins >> at & 1) && there(&v_ok[j], scans >> j & 1)))) {
+                    tc_fence_after();
+                    if (elect_one()) {
+                        if (kb < mine) {
+                            const uint32_t v = smem_u32(ring_v + at * C::KT);
+#pragma unroll
+                            for (int s = 0; s < BN / 16; ++s)
+                                umma_f16_tmem_a(tmem + C::O_COL + i * HD, tmem + (2 * i + (g & 1)) * BN + s * 8,
+                                                smem_desc_mn128(v + s * 2048, BN * 128, 1024), idesc_o, kb > 0 || s > 0);
+                            umma_commit(kb + 1 < mine ? &o_done[i] : &o_full[i]);
+                        }
+                        umma_commit(&v_empty[at]);
+                    }
+                    __syncwarp();
+                    if (j >= 0) ins ^= 1u << at, scans ^= 1u << j;
+                    if (kb < mine) ++g;
+                    ++kb, ++x;
+                    moved = true;
+                }
+            } else if (end) {
+                break;
+            }
+            if (moved) {
+                idle = 0;
+            } else if ((++idle & 31u) == 0) {
+                const uint64_t now = global_ns();
+                if (idle == 32) since = now;
+                bool over = *reinterpret_cast<volatile int*>(&dead) != 0 || now - since > p.timeout_ns;
+                over = __any_sync(0xffffffffu, over);
+                if (over) {
+                    *reinterpret_cast<volatile int*>(&dead) = 1;
+                    break;
+                }
             }
         }
         if (elect_one()) umma_commit(&drain[i]);  // all products are done before the block ends
@@ -440,7 +449,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (it.n == 0) break;
             const int nb = it.all_blocks<NT>(), scan0 = it.scan0();
             // what was noted for the item before is read once its outputs are stored
-            if (k > 0) ok = wait_warp(&q_free[(k - 1) & 1], ((k - 1) >> 1) & 1);
+            if (k > 0) ok = wait_warp(&out_done, (k - 1) & 1);
             if (!scan_sync<C::SCAN>(ok)) break;
             if (*reinterpret_cast<volatile int*>(&odd) == k)
                 for (int d = me; d < HD; d += C::SCAN) first[d] = NONE_BAD;
@@ -489,15 +498,15 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const uint32_t S0 = tmem + lanes + 2 * i * BN, O = tmem + lanes + C::O_COL + i * HD;
         uint32_t scans = 0;
         // g: blocks of this tile so far; done: products with V that were not an item's last; own: items with queries
+        bool ok = true;
         for (int k = 0, g = 0, done = 0, own = 0;; ++k) {
             // the tile's warps take an item, or leave, together: they meet at a barrier below
-            if (!tile_sync(1 + i, item_there(k))) break;
+            if (!tile_sync(1 + i, ok && item_there(k))) break;
             read_item(k, it, true);
             if (it.n == 0) break;
             const int q0 = it.q0(i), s = q0 + row, mine = it.blocks(i), nb = it.all_blocks<NT>(), scan0 = it.scan0();
             float m = -INFINITY, mc = 0.0f;  // the maximum that the exponentials refer to, and times c (0 for -infinity)
             uint64_t sum[4] = {0, 0, 0, 0};  // pairs of partial sums (+0.0)
-            bool ok = true;
             for (int kb = 0; kb < mine; ++kb, ++g) {
                 const uint32_t S = S0 + (g & 1) * BN;
                 ok = wait_warp(&s_full[i][g & 1], (g >> 1) & 1);
@@ -559,9 +568,9 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 tc_fence_before();
                 mbar_arrive(&p_full[i][g & 1]);
             }
-            uint8_t* out = q_tile(k, i);
-            // a tile without queries keeps pace: it must not free the next Q in the place of this one
-            if (mine == 0) ok = wait_warp(&q_full[k & 1], (k >> 1) & 1);
+            // a tile without queries keeps pace with tile 0, which has some in every item: it must not
+            // report the next item's end in the place of this one's
+            if (mine == 0) ok = wait_warp(&o_full[0], k & 1);
             if (mine > 0 && ok) ok = wait_warp(&o_full[i], own & 1);
             // values that are not finite, as noted for the blocks that this tile reads
             for (int kb = scan0; ok && kb < mine; ++kb) ok = wait_warp(&v_ok[kb - scan0], scans >> (kb - scan0) & 1);
@@ -571,19 +580,25 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 const float2 l2 = one_by_one(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
                 const float l = l2.x + l2.y, inv = 1.0f / l;
                 const bool fix = *reinterpret_cast<volatile int*>(&odd) == k + 1;
-                // O / l, rounded, over the Q tile (no product reads it any more), 128-byte swizzle
+                // O / l, rounded, 64 columns at a time through the warp's own shared memory (swizzled like the
+                // tiles), so that 8 lanes write 128 bytes of one row
+                uint8_t* stage = ring_v + C::RV * C::KT + warp * C::OUT;
+                const int row0 = q0 + (warp & 3) * 32, rows = min(32, it.n - row0);
+                T* to = static_cast<T*>(p.o) + (int64_t)(it.start + row0) * p.ld_o + (int64_t)it.head(i) * HD;
 #pragma unroll 1
-                for (int h = 0; h < HD / 32; ++h) {
-                    uint32_t o[32];
-                    tmem_ld_x32(O + 32 * h, o);
+                for (int h = 0; h < HD / 64; ++h) {
+                    uint32_t o[64];
+                    tmem_ld_x32(O + 64 * h, o);
+                    tmem_ld_x32(O + 64 * h + 32, o + 32);
                     tmem_wait_ld_regs(o);
+                    tmem_wait_ld_regs(o + 32);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+                    for (int e = 0; e < 64; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
                     if (fix) {
                         const int at = s - scan0 * BN;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const uint32_t w = *reinterpret_cast<const volatile uint32_t*>(&first[32 * h + e]);
+                        for (int e = 0; e < 64; ++e) {
+                            const uint32_t w = *reinterpret_cast<const volatile uint32_t*>(&first[64 * h + e]);
                             float f = __uint_as_float(o[e]);
                             if (at >= (int)(w & 511u)) f += INFINITY;
                             if (at >= (int)(w >> 9 & 511u)) f -= INFINITY;
@@ -592,41 +607,29 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         }
                     }
 #pragma unroll
-                    for (int g4 = 0; g4 < 4; ++g4) {
+                    for (int e = 0; e < 8; ++e) {
                         uint4 w;
-                        w.x = pack2<T>(__uint_as_float(o[8 * g4]), __uint_as_float(o[8 * g4 + 1]));
-                        w.y = pack2<T>(__uint_as_float(o[8 * g4 + 2]), __uint_as_float(o[8 * g4 + 3]));
-                        w.z = pack2<T>(__uint_as_float(o[8 * g4 + 4]), __uint_as_float(o[8 * g4 + 5]));
-                        w.w = pack2<T>(__uint_as_float(o[8 * g4 + 6]), __uint_as_float(o[8 * g4 + 7]));
-                        const int ch = (h & 1) * 4 + g4;
-                        *reinterpret_cast<uint4*>(out + (h >> 1) * QBOX + row * 128 + ((ch ^ (row & 7)) << 4)) = w;
+                        w.x = pack2<T>(__uint_as_float(o[8 * e]), __uint_as_float(o[8 * e + 1]));
+                        w.y = pack2<T>(__uint_as_float(o[8 * e + 2]), __uint_as_float(o[8 * e + 3]));
+                        w.z = pack2<T>(__uint_as_float(o[8 * e + 4]), __uint_as_float(o[8 * e + 5]));
+                        w.w = pack2<T>(__uint_as_float(o[8 * e + 6]), __uint_as_float(o[8 * e + 7]));
+                        *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = w;
                     }
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int r = 4 * e + (lane >> 3), ch = lane & 7;
+                        if (r < rows)
+                            *reinterpret_cast<uint4*>(to + r * p.ld_o + 64 * h + ch * 8) =
+                                *reinterpret_cast<const uint4*>(stage + r * 128 + ((ch ^ (r & 7)) << 4));
+                    }
+                    __syncwarp();
                 }
                 tc_fence_before();  // the next item's products write over O
                 if (s < it.n && p.lse != nullptr) p.lse[(int64_t)it.head(i) * p.rows + it.start + s] = (mc + log2f(l)) * LN2;
-                fence_proxy_async_smem();
-            }
-            if (!tile_sync(1 + i, ok)) break;
-            if (mine > 0) {
-                const int rows = min(BM, it.n - q0);
-                if (rows == BM) {
-                    if (row == 0) {
-                        for (int h = 0; h < HD / 64; ++h) tma_store_2d(&tm_o, out + h * QBOX, it.head(i) * HD + 64 * h, it.start + q0);
-                        bulk_commit();
-                        bulk_wait_read<0>();
-                    }
-                } else {
-                    constexpr int PER = HD / 8;  // 16-byte pieces of a row
-                    for (int y = row; y < rows * PER; y += 128) {
-                        const int r = y / PER, ch = y % PER;
-                        const uint4 w = *reinterpret_cast<const uint4*>(out + (ch >> 3) * QBOX + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
-                        *reinterpret_cast<uint4*>(static_cast<T*>(p.o) + (int64_t)(it.start + q0 + r) * p.ld_o + (int64_t)it.head(i) * HD + ch * 8) = w;
-                    }
-                }
                 done += mine - 1, ++own;
             }
-            fence_proxy_async_smem();  // what was read here is loaded over next
-            mbar_arrive(&q_free[k & 1]);
+            mbar_arrive(&out_done);
         }
     }
     __syncwarp();
@@ -659,12 +662,11 @@ static cudaError_t prompt_tc(const PromptArgs& p, cudaStream_t st) {
     using C = TCfg<HD, NT>;
     constexpr int SMEM = C::TILES + (int)sizeof(Aux<HD, NT>);
     static_assert(C::CTAS * (SMEM + 1024) <= 228 * 1024, "the blocks of an SM share its memory");
-    CUtensorMap q, k, v, o;
+    CUtensorMap q, k, v;
     const int64_t wq = (int64_t)p.n_heads * HD, wk = (int64_t)p.n_kv * HD;
     cudaError_t e = rows_map(&q, p.dtype, p.q, wq, p.rows, p.ld_q, BM);
     if (e == cudaSuccess) e = rows_map(&k, p.dtype, p.k, wk, p.rows, p.ld_k, BN);
     if (e == cudaSuccess) e = rows_map(&v, p.dtype, p.v, wk, p.rows, p.ld_v, BN);
-    if (e == cudaSuccess) e = rows_map(&o, p.dtype, p.o, wq, p.rows, p.ld_o, BM);
     if (e == cudaSuccess) e = prepare_smem((const void*)prompt_tc_kernel<T, HD, NT>, SMEM);
     if (e != cudaSuccess) return e;
     PromptTcArgs a;
@@ -675,7 +677,7 @@ static cudaError_t prompt_tc(const PromptArgs& p, cudaStream_t st) {
     const int most = p.rows / tile + (p.batch < p.rows ? p.batch : p.rows);
     a.head_steps = a.pair_heads ? p.n_heads / 2 : p.n_heads;
     const dim3 grid(most, a.head_steps);
-    prompt_tc_kernel<T, HD, NT><<<grid, C::THREADS, SMEM, st>>>(q, k, v, o, a);
+    prompt_tc_kernel<T, HD, NT><<<grid, C::THREADS, SMEM, st>>>(q, k, v, a);
     return cudaGetLastError();
 }
 
