@@ -3,20 +3,30 @@
 //
 //   o_j(s) = sum_{t <= s} exp(c q_j(s) . k(t) - lse_j(s)) v(t)
 //
-// A block holds NT tiles of 128 queries that read the same keys: two query heads of one kv head
-// where a kv head has an even number of them, else neighbouring tiles of one head.  Keys and
-// values pass by in blocks of BN, one pass with a running maximum and sum:
-//   loader     one thread: Q tiles, then K and V blocks into a ring of buffers by TMA
-//   products   one thread: S_i = Q_i K^T into TMEM, O_i += P_i V with P_i read from TMEM (over the
-//              columns of S_i).  Tile 1's products run while tile 0's softmax does, and the other
-//              way round.
-//   softmax    four warps per tile, a thread per query: row of S to registers, maximum,
-//              exponentials, P rounded to 16 bits back to TMEM.  O is rescaled only when the
-//              maximum grew by more than 2^8: until then the exponentials are at most 2^8, in
-//              range of both types, and the common factor leaves with the sum.
+// An item is a tile of 128 queries of one (sequence, head).  Its keys and values pass by once in blocks
+// of 64, with a running maximum and sum:
+//   loader     one warp: announces the items, loads Q tiles and K and V blocks by TMA
+//   products   one warp: S = Q K^T into TMEM (two buffers, up to two blocks ahead), O += P V with P
+//              read from TMEM (over the columns of S)
+//   softmax    four warps, a thread per query: row of S to registers, maximum, exponentials, P rounded to
+//              16 bits back to TMEM.  O is rescaled only when the maximum grew by more than 2^8:
+//              until then the exponentials are at most 2^8, in range of both types, and the common
+//              factor leaves with the sum.
 //   scan       two warps: rows of V behind the sequence and values that are not finite are
 //              zeroed in the blocks that cross the diagonal (there 0 * NaN would reach earlier
 //              rows); the latter are noted and added to the rows that see them at the end.
+// Two blocks share an SM, so that one's softmax runs under the other's products.  A block that is done with
+// an item takes the next one of a block that has not started (cluster launch control): the loads
+// and scores of the next item overlap the end of this one, and the hardware keeps balancing the load.
+// On 64 requests of 1 to 256 tokens that took 172 us where a block per item took 277.
+//
+// One prompt of 8192 tokens, 32 heads of 128, 8 kv heads, bf16: 455 us, 1210 TFLOP/s, 0.88 of the
+// sustained rate of a library matrix product here.  A step of 64 keys needs 620
+// cycles of the tensor cores (384 for the scores, which read both operands from shared memory, 256 for the
+// products with V) and 512 of the special function units (64 x 128 exponentials at 16 a cycle); taking a quarter of
+// the exponentials on the FMA pipe measured slower.  Tried and slower: 128 keys per block with one buffer of
+// scores (528 us), two tiles per block that share K and V (448 us there and 6 % faster with 96 kv heads, but 10 to
+// 70 % slower on prompts below 128 tokens).
 #include <cudaTypedefs.h>
 #include <math.h>
 
@@ -36,22 +46,21 @@ constexpr float GROW = 8.0f;            // log2 of the growth that the running m
 
 constexpr int BN = 64;                  // keys per block
 
-template <int HD, int NT>
+constexpr int SOFT = 4;                 // softmax warps; then the loader's, the products' and those that scan
+constexpr int SCAN = 64;                // threads that scan V
+constexpr int THREADS = SOFT * 32 + 64 + SCAN;
+constexpr int READERS = SOFT + 1 + SCAN / 32;  // warps that follow the items
+constexpr int SCANS = BM / BN;          // most blocks that cross the diagonal
+constexpr int O_COL = 2 * BN;           // TMEM: two buffers of S, then O
+constexpr int OUT = 32 * 128;           // bytes of a softmax warp's outputs on their way out
+
+template <int HD>
 struct TCfg {
-    static constexpr int QT = HD / 64 * QBOX;                // bytes of a Q tile
-    static constexpr int KT = HD * BN * 2;                   // bytes of a K or V block
-    // buffers of K and of V; 4 KB for each softmax warp's outputs
-    static constexpr int RK = NT == 2 ? (HD == 128 ? 4 : 8) : (HD == 128 ? 2 : 4);
-    static constexpr int RV = RK;
-    static constexpr int OUT = 32 * 128;
-    static constexpr int TILES = NT * QT + (RK + RV) * KT + NT * 4 * OUT;
-    static constexpr int THREADS = NT * 128 + 128;
-    static constexpr int SCAN = NT == 2 ? 32 : 64;           // threads that scan V
-    static constexpr int O_COL = NT * 2 * BN;                // S takes two buffers per tile
-    static constexpr int TMEM = NT == 2 ? 512 : 256;
-    static constexpr int CTAS = NT == 2 ? 1 : 2;
-    static constexpr int SCANS = NT * BM / BN;               // most blocks that cross a diagonal
-    static constexpr int READERS = NT * 4 + NT + SCAN / 32;  // warps that follow the items
+    static constexpr int QT = HD / 64 * QBOX;         // bytes of a Q tile
+    static constexpr int KT = HD * BN * 2;            // bytes of a K or V block
+    static constexpr int RING = HD == 128 ? 2 : 4;    // buffers of K, and of V
+    static constexpr int TILES = QT + 2 * RING * KT + SOFT * OUT;
+    static constexpr int TMEM = 256;
 };
 constexpr int ITEMS = 4;  // items that the loader announces ahead
 
@@ -73,16 +82,16 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
         "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
-// Barrier of a tile's 128 softmax threads; true in all of them if `ok` is in all.
-__device__ __forceinline__ bool tile_sync(int id, bool ok) {
+// Barrier of the softmax threads; true in all of them if `ok` is in all.
+__device__ __forceinline__ bool softmax_sync(bool ok) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %2, 0;\n\t"
-        "bar.red.and.pred q, %1, 128, p;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.and.pred q, 1, %2, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"(id), "r"((uint32_t)ok)
+        : "r"((uint32_t)ok), "n"(SOFT * 32)
         : "memory");
     return r != 0;
 }
@@ -151,19 +160,17 @@ __device__ __forceinline__ float max_of(const uint32_t* x) {
 
 struct PromptTcArgs {
     PromptArgs p;
-    int pair_heads;  // NT == 2: the tiles are two heads of one kv head
-    int head_steps;  // heads, or pairs of them
     float c;         // scale * log2(e)
 };
 
 // What a block's warps share beside the tiles.
-template <int HD, int NT>
+template <int HD>
 struct Aux {
-    using C = TCfg<HD, NT>;
-    uint64_t q_full, q_empty, out_done, o_done[NT], o_full[NT], drain[NT], s_full[NT][2], p_full[NT][2];
-    uint64_t k_full[C::RK], k_empty[C::RK], v_full[C::RV], v_empty[C::RV];
-    uint64_t v_in[C::RV];     // a block that is scanned has landed in this buffer
-    uint64_t v_ok[C::SCANS];  // an item's first, second, ... such block is scanned
+    using C = TCfg<HD>;
+    uint64_t q_full, q_empty, out_done, o_done, o_full, drain, s_full[2], p_full[2];
+    uint64_t k_full[C::RING], k_empty[C::RING], v_full[C::RING], v_empty[C::RING];
+    uint64_t v_in[C::RING];     // a block that is scanned has landed in this buffer
+    uint64_t v_ok[SCANS];  // an item's first, second, ... such block is scanned
     uint64_t item_full[ITEMS], item_empty[ITEMS], answer_bar, pad;
     int4 items[ITEMS];
     uint4 answer;
@@ -174,24 +181,19 @@ struct Aux {
 
 // One work item of a block.
 struct PromptItem {
-    int start, n, blk, head0;  // first row and length of the sequence, tile, first query head; n = 0: no more items
-    int pair, rows;            // rows that an item's tiles cover
-    __device__ __forceinline__ int q0(int i) const { return blk * rows + (pair ? 0 : i * BM); }
-    __device__ __forceinline__ int head(int i) const { return head0 + (pair ? i : 0); }
-    // key blocks of tile i (0: the tile has no queries), and of the item
-    __device__ __forceinline__ int blocks(int i) const { return q0(i) < n ? (min(n, q0(i) + BM) + BN - 1) / BN : 0; }
-    template <int NT>
-    __device__ __forceinline__ int all_blocks() const { return NT == 1 ? blocks(0) : max(blocks(0), blocks(1)); }
-    __device__ __forceinline__ int scan0() const { return q0(0) / BN; }  // first block with keys behind a query
+    int start, n, blk, head;  // first row and length of the sequence, tile, query head; n = 0: no more items
+    __device__ __forceinline__ int q0() const { return blk * BM; }
+    __device__ __forceinline__ int blocks() const { return (min(n, q0() + BM) + BN - 1) / BN; }  // of keys
+    __device__ __forceinline__ int scan0() const { return q0() / BN; }  // first block with keys behind a query
 };
 
-template <typename T, int HD, int NT>
-__global__ void __launch_bounds__(TCfg<HD, NT>::THREADS, TCfg<HD, NT>::CTAS)
+template <typename T, int HD>
+__global__ void __launch_bounds__(THREADS, 2)
 prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const PromptTcArgs a) {
-    using C = TCfg<HD, NT>;
+    using C = TCfg<HD>;
     extern __shared__ __align__(1024) uint8_t base[];  // the tiles, swizzled in units of 1024 bytes, then Aux
-    Aux<HD, NT>& aux = *reinterpret_cast<Aux<HD, NT>*>(base + C::TILES);
+    Aux<HD>& aux = *reinterpret_cast<Aux<HD>*>(base + C::TILES);
     auto& q_full = aux.q_full;
     auto& q_empty = aux.q_empty;
     auto& out_done = aux.out_done;
@@ -218,26 +220,23 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const PromptArgs& p = a.p;
     if (stopped(p.status)) return;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const int tile_rows = NT == 2 && !a.pair_heads ? 2 * BM : BM;
 
-    uint8_t* ring_k = base + NT * C::QT;
-    uint8_t* ring_v = ring_k + C::RK * C::KT;
-    for (int i = tid; i < HD; i += C::THREADS) first[i] = NONE_BAD;
+    uint8_t* ring_k = base + C::QT;
+    uint8_t* ring_v = ring_k + C::RING * C::KT;
+    for (int i = tid; i < HD; i += THREADS) first[i] = NONE_BAD;
     if (tid == 0) {
-        mbar_init(&q_full, 1), mbar_init(&q_empty, NT), mbar_init(&out_done, NT * 128);
-        for (int i = 0; i < NT; ++i) {
-            mbar_init(&o_done[i], 1), mbar_init(&o_full[i], 1), mbar_init(&drain[i], 1);
-            for (int y = 0; y < 2; ++y) mbar_init(&s_full[i][y], 1), mbar_init(&p_full[i][y], 128);
-        }
-        for (int i = 0; i < C::RK; ++i) mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], NT);
-        for (int i = 0; i < C::RV; ++i) mbar_init(&v_full[i], 1), mbar_init(&v_empty[i], NT), mbar_init(&v_in[i], 1);
-        for (int i = 0; i < C::SCANS; ++i) mbar_init(&v_ok[i], C::SCAN);
-        for (int i = 0; i < ITEMS; ++i) mbar_init(&item_full[i], 1), mbar_init(&item_empty[i], C::READERS);
+        mbar_init(&q_full, 1), mbar_init(&q_empty, 1), mbar_init(&out_done, SOFT * 32);
+        mbar_init(&o_done, 1), mbar_init(&o_full, 1), mbar_init(&drain, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_full[i], SOFT * 32);
+        for (int i = 0; i < C::RING; ++i)
+            mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], 1), mbar_init(&v_full[i], 1), mbar_init(&v_empty[i], 1), mbar_init(&v_in[i], 1);
+        for (int i = 0; i < SCANS; ++i) mbar_init(&v_ok[i], SCAN);
+        for (int i = 0; i < ITEMS; ++i) mbar_init(&item_full[i], 1), mbar_init(&item_empty[i], READERS);
         mbar_init(&answer_bar, 1);
         dead = smem_u32(base) % 1024 != 0, odd = 0;
         fence_mbar_init();
     }
-    if (warp == NT * 4) {
+    if (warp == SOFT) {
         tmem_alloc(&tmem_slot, C::TMEM);
         tmem_relinquish();
     }
@@ -253,23 +252,23 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     // TMEM is read, and work is issued, by whole warps: their lanes give up together
     auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
     PromptItem it;
-    it.pair = a.pair_heads, it.rows = tile_rows;
     // Item k of this block; false where a wait ran out.  `leave`: this warp needs it no more.
     auto read_item = [&](int k, PromptItem& to, bool leave) {
         const int at = k % ITEMS;
         const volatile int4& v = items[at];
         const int4 w = make_int4(v.x, v.y, v.z, v.w);
-        to.start = w.x, to.n = w.y, to.blk = w.z, to.head0 = w.w;
+        to.start = w.x, to.n = w.y, to.blk = w.z, to.head = w.w;
         __syncwarp();
         if (leave && lane == 0) mbar_arrive(&item_empty[at]);
     };
     auto item_there = [&](int k) { return wait_warp(&item_full[k % ITEMS], (k / ITEMS) & 1); };
 
-    if (warp == NT * 4) {
+    if (warp == SOFT) {
         // ---- loader: announces the items, loads Q, then K(0), K(1), V(0), K(2), V(1), ... of each
         int x = blockIdx.x, y = blockIdx.y, k = 0, nk = 0, nv = 0, asked = 0;
         uint32_t ins = 0;  // bit i: parity of v_in[i]'s next use
         bool ok = dead == 0, more = true;
+        if (lane == 0) tma_prefetch_desc(&tm_q), tma_prefetch_desc(&tm_k), tma_prefetch_desc(&tm_v);
         auto announce = [&](int4 w) {
             const int at = k % ITEMS;
             if (k >= ITEMS) ok = wait_warp(&item_empty[at], (k / ITEMS - 1) & 1);
@@ -290,26 +289,24 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             auto count = [&](int i) {
                 int s, len;
                 seq_rows(p.cu, i, p.rows, s, len);
-                return (len + tile_rows - 1) / tile_rows;
+                return (len + BM - 1) / BM;
             };
-            if (find_item(p.batch, (int)(lin / a.head_steps), count, b, blk)) {
+            if (find_item(p.batch, (int)(lin / p.n_heads), count, b, blk)) {
                 seq_rows(p.cu, b, p.rows, it.start, it.n);
-                it.blk = (it.n + tile_rows - 1) / tile_rows - 1 - blk;  // the longest rows first
-                it.head0 = (int)(lin % a.head_steps) * (a.pair_heads ? 2 : 1);
-                announce(make_int4(it.start, it.n, it.blk, it.head0));
-                const int kvh = it.head0 / (p.n_heads / p.n_kv), nb = it.all_blocks<NT>(), scan0 = it.scan0();
+                it.blk = (it.n + BM - 1) / BM - 1 - blk;  // the longest rows first
+                it.head = (int)(lin % p.n_heads);
+                announce(make_int4(it.start, it.n, it.blk, it.head));
+                const int kvh = it.head / (p.n_heads / p.n_kv), nb = it.blocks(), scan0 = it.scan0();
                 if (ok && k >= 1) ok = wait_warp(&q_empty, (k - 1) & 1);
                 if (ok && elect_one()) {
-                    const int tiles = NT == 2 && it.blocks(NT - 1) > 0 ? NT : 1;
-                    mbar_arrive_expect_tx(&q_full, tiles * C::QT);
-                    for (int i = 0; i < tiles; ++i)
-                        for (int h = 0; h < HD / 64; ++h)
-                            tma_load_2d(base + i * C::QT + h * QBOX, &tm_q, &q_full, it.head(i) * HD + 64 * h, it.start + it.q0(i));
+                    mbar_arrive_expect_tx(&q_full, C::QT);
+                    for (int h = 0; h < HD / 64; ++h)
+                        tma_load_2d(base + h * QBOX, &tm_q, &q_full, it.head * HD + 64 * h, it.start + it.q0());
                 }
                 for (int ik = 0, iv = 0; ok && iv < nb;) {
                     const bool keys = ik < nb && ik - iv < 2;
-                    const int kb = keys ? ik : iv, g = keys ? nk : nv, ring = keys ? C::RK : C::RV, at = g % ring;
-                    if (g >= ring) ok = wait_warp(keys ? &k_empty[at] : &v_empty[at], (g / ring - 1) & 1);
+                    const int kb = keys ? ik : iv, g = keys ? nk : nv, at = g % C::RING;
+                    if (g >= C::RING) ok = wait_warp(keys ? &k_empty[at] : &v_empty[at], (g / C::RING - 1) & 1);
                     if (!ok) break;
                     if (elect_one()) {
                         uint64_t* bar = keys ? &k_full[at] : &v_full[at];
@@ -341,25 +338,23 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         if (ok) announce(make_int4(0, 0, 0, 0));
         // All copies have landed before the block ends, also where a wait ran out.
         if (k > 0) mbar_wait_bounded(&q_full, (k - 1) & 1, nullptr, p.timeout_ns);
-        for (int g = max(0, nk - C::RK); g < nk; ++g) mbar_wait_bounded(&k_full[g % C::RK], (g / C::RK) & 1, nullptr, p.timeout_ns);
-        for (int g = max(0, nv - C::RV); g < nv; ++g) mbar_wait_bounded(&v_full[g % C::RV], (g / C::RV) & 1, nullptr, p.timeout_ns);
-        for (int i = 0; i < C::RV; ++i)  // (an unused one passes: the phase before its first counts as done)
+        for (int g = max(0, nk - C::RING); g < nk; ++g) mbar_wait_bounded(&k_full[g % C::RING], (g / C::RING) & 1, nullptr, p.timeout_ns);
+        for (int g = max(0, nv - C::RING); g < nv; ++g) mbar_wait_bounded(&v_full[g % C::RING], (g / C::RING) & 1, nullptr, p.timeout_ns);
+        for (int i = 0; i < C::RING; ++i)  // (an unused one passes: the phase before its first counts as done)
             mbar_wait_bounded(&v_in[i], (ins >> i & 1) ^ 1, nullptr, p.timeout_ns);
-    } else if (warp > NT * 4 && warp <= NT * 4 + NT) {
-        // ---- products of tile i: the whole warp follows, one lane issues.  A warp per tile: one's
-        // products fill the time in which the other looks at its barriers.  The scores run up to two blocks
+    } else if (warp == SOFT + 1) {
+        // ---- products: the whole warp follows, one lane issues.  The scores run up to two blocks
         // ahead of the products with V, over the ends of items; whichever of the two can go on does (the
         // next item's Q may still be on its way when the last products of this one are due).
         constexpr uint32_t fmt = std::is_same<T, __half>::value ? 0u : 1u;
         constexpr uint32_t idesc_s = idesc_f16(fmt, BM, BN, 0), idesc_o = idesc_f16(fmt, BM, HD, 1);
-        const int i = warp - NT * 4 - 1;
         auto there = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_wait(bar, parity)) != 0; };
-        // the scores: item, its block, K block and own block in all; has: the item is read
+        // the scores: item, its block, block in all; has: the item is read
         PromptItem ahead = it;
-        int a_item = 0, a_kb = 0, a_nb = 0, a_mine = 0, a_x = 0, a_g = 0;
+        int a_item = 0, a_kb = 0, a_nb = 0, a_x = 0;
         bool end = false, has = false;
         // the products with V: the same
-        int k = 0, kb = 0, nb = 0, mine = 0, scan0 = 0, x = 0, g = 0;
+        int k = 0, kb = 0, nb = 0, scan0 = 0, x = 0;
         uint32_t ins = 0, scans = 0;  // parities of the next uses of v_in, v_ok
         uint64_t since = 0;
         for (uint32_t idle = 0;;) {
@@ -368,26 +363,23 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 read_item(a_item, ahead, false);
                 end = ahead.n == 0;
                 has = !end;
-                a_nb = ahead.all_blocks<NT>(), a_mine = ahead.blocks(i), a_kb = 0;
+                a_nb = ahead.blocks(), a_kb = 0;
             }
-            const int ka = a_x % C::RK;
+            const int ka = a_x % C::RING;
             // (over the scores of the block two before: its products come first)
-            if (has && a_x - x < 2 && (a_kb > 0 || there(&q_full, a_item & 1)) && there(&k_full[ka], (a_x / C::RK) & 1)) {
+            if (has && a_x - x < 2 && (a_kb > 0 || there(&q_full, a_item & 1)) && there(&k_full[ka], (a_x / C::RING) & 1)) {
                 tc_fence_after();
                 if (elect_one()) {
-                    if (a_kb < a_mine) {
-                        const uint32_t q = smem_u32(base + i * C::QT), kk = smem_u32(ring_k + ka * C::KT);
+                    const uint32_t q = smem_u32(base), kk = smem_u32(ring_k + ka * C::KT);
 #pragma unroll
-                        for (int s = 0; s < HD / 16; ++s)
-                            umma_f16(tmem + (2 * i + (a_g & 1)) * BN, smem_desc_k128(q + (s >> 2) * QBOX) + 2 * (s & 3),
-                                     smem_desc_k128(kk + (s >> 2) * BN * 128) + 2 * (s & 3), idesc_s, s > 0);
-                        umma_commit(&s_full[i][a_g & 1]);
-                    }
+                    for (int s = 0; s < HD / 16; ++s)
+                        umma_f16(tmem + (a_x & 1) * BN, smem_desc_k128(q + (s >> 2) * QBOX) + 2 * (s & 3),
+                                 smem_desc_k128(kk + (s >> 2) * BN * 128) + 2 * (s & 3), idesc_s, s > 0);
+                    umma_commit(&s_full[a_x & 1]);
                     umma_commit(&k_empty[ka]);  // K's buffer is free once they are done, and after an item's last ones Q's
                     if (a_kb + 1 == a_nb) umma_commit(&q_empty);
                 }
                 __syncwarp();
-                if (a_kb < a_mine) ++a_g;
                 ++a_x;
                 if (++a_kb == a_nb) has = false, ++a_item;
                 moved = true;
@@ -395,26 +387,23 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (x < a_x) {  // its scores are under way, so its item was announced
                 if (kb == nb) {
                     read_item(k, it, true);
-                    nb = it.all_blocks<NT>(), mine = it.blocks(i), scan0 = it.scan0(), kb = 0, ++k;
+                    nb = it.blocks(), scan0 = it.scan0(), kb = 0, ++k;
                 }
-                const int at = x % C::RV, j = kb - scan0;
-                if ((kb >= mine || there(&p_full[i][g & 1], (g >> 1) & 1)) && there(&v_full[at], (x / C::RV) & 1) &&
+                const int at = x % C::RING, j = kb - scan0;
+                if (there(&p_full[x & 1], (x >> 1) & 1) && there(&v_full[at], (x / C::RING) & 1) &&
                     (j < 0 || (there(&v_in[at], ins >> at & 1) && there(&v_ok[j], scans >> j & 1)))) {
                     tc_fence_after();
                     if (elect_one()) {
-                        if (kb < mine) {
-                            const uint32_t v = smem_u32(ring_v + at * C::KT);
+                        const uint32_t v = smem_u32(ring_v + at * C::KT);
 #pragma unroll
-                            for (int s = 0; s < BN / 16; ++s)
-                                umma_f16_tmem_a(tmem + C::O_COL + i * HD, tmem + (2 * i + (g & 1)) * BN + s * 8,
-                                                smem_desc_mn128(v + s * 2048, BN * 128, 1024), idesc_o, kb > 0 || s > 0);
-                            umma_commit(kb + 1 < mine ? &o_done[i] : &o_full[i]);
-                        }
+                        for (int s = 0; s < BN / 16; ++s)
+                            umma_f16_tmem_a(tmem + O_COL, tmem + (x & 1) * BN + s * 8, smem_desc_mn128(v + s * 2048, BN * 128, 1024),
+                                            idesc_o, kb > 0 || s > 0);
+                        umma_commit(kb + 1 < nb ? &o_done : &o_full);
                         umma_commit(&v_empty[at]);
                     }
                     __syncwarp();
                     if (j >= 0) ins ^= 1u << at, scans ^= 1u << j;
-                    if (kb < mine) ++g;
                     ++kb, ++x;
                     moved = true;
                 }
@@ -434,33 +423,33 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 }
             }
         }
-        if (elect_one()) umma_commit(&drain[i]);  // all products are done before the block ends
-        mbar_wait_bounded(&drain[i], 0, nullptr, p.timeout_ns);
-    } else if (warp > NT * 4 + NT) {
+        if (elect_one()) umma_commit(&drain);  // all products are done before the block ends
+        mbar_wait_bounded(&drain, 0, nullptr, p.timeout_ns);
+    } else if (warp > SOFT + 1) {
         // ---- scan of V
         constexpr uint32_t INF = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
-        const int me = tid - (NT * 4 + NT + 1) * 32;
+        const int me = tid - (SOFT + 2) * 32;
         uint32_t ins = 0;
         bool ok = true;
         for (int k = 0, x = 0;; ++k) {
             // (its warps leave together: they meet at barriers)
-            if (!scan_sync<C::SCAN>(ok && item_there(k))) break;
+            if (!scan_sync<SCAN>(ok && item_there(k))) break;
             read_item(k, it, true);
             if (it.n == 0) break;
-            const int nb = it.all_blocks<NT>(), scan0 = it.scan0();
+            const int nb = it.blocks(), scan0 = it.scan0();
             // what was noted for the item before is read once its outputs are stored
             if (k > 0) ok = wait_warp(&out_done, (k - 1) & 1);
-            if (!scan_sync<C::SCAN>(ok)) break;
+            if (!scan_sync<SCAN>(ok)) break;
             if (*reinterpret_cast<volatile int*>(&odd) == k)
-                for (int d = me; d < HD; d += C::SCAN) first[d] = NONE_BAD;
-            scan_sync<C::SCAN>(true);
+                for (int d = me; d < HD; d += SCAN) first[d] = NONE_BAD;
+            scan_sync<SCAN>(true);
             for (int kb = scan0; kb < nb; ++kb) {
-                const int at = (x + kb) % C::RV;
+                const int at = (x + kb) % C::RING;
                 ok = wait_warp(&v_in[at], ins >> at & 1);
                 ins ^= 1u << at;
                 if (!ok) break;
                 uint8_t* v = ring_v + at * C::KT;
-                for (int r = me; r < BN; r += C::SCAN) {
+                for (int r = me; r < BN; r += SCAN) {
                     const int t = kb * BN + r;
                     uint32_t most = 0;
                     if (t < it.n) {
@@ -492,24 +481,23 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             x += nb;
         }
     } else {
-        // ---- softmax of tile i, one query per thread
-        const int i = NT == 2 ? warp >> 2 : 0, row = tid & 127;
-        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t S0 = tmem + lanes + 2 * i * BN, O = tmem + lanes + C::O_COL + i * HD;
+        // ---- softmax, one query per thread
+        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        const uint32_t S0 = tmem + lanes, O = tmem + lanes + O_COL;
         uint32_t scans = 0;
-        // g: blocks of this tile so far; done: products with V that were not an item's last; own: items with queries
+        // g: blocks so far; done: products with V that were not an item's last
         bool ok = true;
-        for (int k = 0, g = 0, done = 0, own = 0;; ++k) {
-            // the tile's warps take an item, or leave, together: they meet at a barrier below
-            if (!tile_sync(1 + i, ok && item_there(k))) break;
+        for (int k = 0, g = 0, done = 0;; ++k) {
+            // the warps take an item, or leave, together: they meet at a barrier below
+            if (!softmax_sync(ok && item_there(k))) break;
             read_item(k, it, true);
             if (it.n == 0) break;
-            const int q0 = it.q0(i), s = q0 + row, mine = it.blocks(i), nb = it.all_blocks<NT>(), scan0 = it.scan0();
+            const int q0 = it.q0(), s = q0 + tid, nb = it.blocks(), scan0 = it.scan0();
             float m = -INFINITY, mc = 0.0f;  // the maximum that the exponentials refer to, and times c (0 for -infinity)
             uint64_t sum[4] = {0, 0, 0, 0};  // pairs of partial sums (+0.0)
-            for (int kb = 0; kb < mine; ++kb, ++g) {
+            for (int kb = 0; kb < nb; ++kb, ++g) {
                 const uint32_t S = S0 + (g & 1) * BN;
-                ok = wait_warp(&s_full[i][g & 1], (g >> 1) & 1);
+                ok = wait_warp(&s_full[g & 1], (g >> 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
                 uint32_t x[BN];
@@ -530,7 +518,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 } else if (__any_sync(0xffffffffu, (mx - m) * a.c > GROW)) {
                     // O is at rest once the products of block kb - 1 are done; those of kb - 2 were before S,
                     // those of kb wait for this thread: the phase is the barrier's current or last one
-                    ok = wait_warp(&o_done[i], (done + kb - 1) & 1);
+                    ok = wait_warp(&o_done, (done + kb - 1) & 1);
                     if (!ok) break;
                     tc_fence_after();
                     float by = 1.0f;
@@ -566,25 +554,22 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(&p_full[i][g & 1]);
+                mbar_arrive(&p_full[g & 1]);
             }
-            // a tile without queries keeps pace with tile 0, which has some in every item: it must not
-            // report the next item's end in the place of this one's
-            if (mine == 0) ok = wait_warp(&o_full[0], k & 1);
-            if (mine > 0 && ok) ok = wait_warp(&o_full[i], own & 1);
-            // values that are not finite, as noted for the blocks that this tile reads
-            for (int kb = scan0; ok && kb < mine; ++kb) ok = wait_warp(&v_ok[kb - scan0], scans >> (kb - scan0) & 1);
+            if (ok) ok = wait_warp(&o_full, k & 1);
+            // values that are not finite, as noted by the scan
+            for (int kb = scan0; ok && kb < nb; ++kb) ok = wait_warp(&v_ok[kb - scan0], scans >> (kb - scan0) & 1);
             for (int kb = scan0; kb < nb; ++kb) scans ^= 1u << (kb - scan0);
-            if (mine > 0 && ok) {
+            if (ok) {
                 tc_fence_after();
                 const float2 l2 = one_by_one(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
                 const float l = l2.x + l2.y, inv = 1.0f / l;
                 const bool fix = *reinterpret_cast<volatile int*>(&odd) == k + 1;
                 // O / l, rounded, 64 columns at a time through the warp's own shared memory (swizzled like the
                 // tiles), so that 8 lanes write 128 bytes of one row
-                uint8_t* stage = ring_v + C::RV * C::KT + warp * C::OUT;
-                const int row0 = q0 + (warp & 3) * 32, rows = min(32, it.n - row0);
-                T* to = static_cast<T*>(p.o) + (int64_t)(it.start + row0) * p.ld_o + (int64_t)it.head(i) * HD;
+                uint8_t* stage = ring_v + C::RING * C::KT + warp * OUT;
+                const int row0 = q0 + warp * 32, rows = min(32, it.n - row0);
+                T* to = static_cast<T*>(p.o) + (int64_t)(it.start + row0) * p.ld_o + (int64_t)it.head * HD;
 #pragma unroll 1
                 for (int h = 0; h < HD / 64; ++h) {
                     uint32_t o[64];
@@ -626,8 +611,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     __syncwarp();
                 }
                 tc_fence_before();  // the next item's products write over O
-                if (s < it.n && p.lse != nullptr) p.lse[(int64_t)it.head(i) * p.rows + it.start + s] = (mc + log2f(l)) * LN2;
-                done += mine - 1, ++own;
+                if (s < it.n && p.lse != nullptr) p.lse[(int64_t)it.head * p.rows + it.start + s] = (mc + log2f(l)) * LN2;
+                done += nb - 1;
             }
             mbar_arrive(&out_done);
         }
@@ -637,7 +622,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     __syncthreads();
     tc_fence_after();
     if (tid == 0 && dead) status_or(p.status, ENERGON_DEVICE_TIMEOUT);
-    if (warp == NT * 4) tmem_dealloc(tmem, C::TMEM);
+    if (warp == SOFT) tmem_dealloc(tmem, C::TMEM);
 }
 
 // ------------------------------------------------------------------ host side
@@ -657,39 +642,31 @@ cudaError_t rows_map(CUtensorMap* m, int dtype, const void* ptr, int64_t cols, i
                : cudaErrorInvalidValue;
 }
 
-template <typename T, int HD, int NT>
+template <typename T, int HD>
 static cudaError_t prompt_tc(const PromptArgs& p, cudaStream_t st) {
-    using C = TCfg<HD, NT>;
-    constexpr int SMEM = C::TILES + (int)sizeof(Aux<HD, NT>);
-    static_assert(C::CTAS * (SMEM + 1024) <= 228 * 1024, "the blocks of an SM share its memory");
+    using C = TCfg<HD>;
+    constexpr int SMEM = C::TILES + (int)sizeof(Aux<HD>);
+    static_assert(2 * (SMEM + 1024) <= 228 * 1024, "the blocks of an SM share its memory");
     CUtensorMap q, k, v;
     const int64_t wq = (int64_t)p.n_heads * HD, wk = (int64_t)p.n_kv * HD;
     cudaError_t e = rows_map(&q, p.dtype, p.q, wq, p.rows, p.ld_q, BM);
     if (e == cudaSuccess) e = rows_map(&k, p.dtype, p.k, wk, p.rows, p.ld_k, BN);
     if (e == cudaSuccess) e = rows_map(&v, p.dtype, p.v, wk, p.rows, p.ld_v, BN);
-    if (e == cudaSuccess) e = prepare_smem((const void*)prompt_tc_kernel<T, HD, NT>, SMEM);
+    if (e == cudaSuccess) e = prepare_smem((const void*)prompt_tc_kernel<T, HD>, SMEM);
     if (e != cudaSuccess) return e;
     PromptTcArgs a;
     a.p = p;
-    a.pair_heads = NT == 2 && p.n_heads / p.n_kv % 2 == 0;
     a.c = p.scale * LOG2E;
-    const int tile = NT == 2 && !a.pair_heads ? 2 * BM : BM;
-    const int most = p.rows / tile + (p.batch < p.rows ? p.batch : p.rows);
-    a.head_steps = a.pair_heads ? p.n_heads / 2 : p.n_heads;
-    const dim3 grid(most, a.head_steps);
-    prompt_tc_kernel<T, HD, NT><<<grid, C::THREADS, SMEM, st>>>(q, k, v, a);
+    const int most = p.rows / BM + (p.batch < p.rows ? p.batch : p.rows);
+    const dim3 grid(most, p.n_heads);  // (heads pass by first: see the kernel)
+    prompt_tc_kernel<T, HD><<<grid, THREADS, SMEM, st>>>(q, k, v, a);
     return cudaGetLastError();
 }
 
-template <typename T>
-static cudaError_t prompt_tc_t(const PromptArgs& p, cudaStream_t st) {
-    const bool two_tiles = p.rows / p.batch > 256;
-    if (p.head_dim == 64) return two_tiles ? prompt_tc<T, 64, 2>(p, st) : prompt_tc<T, 64, 1>(p, st);
-    return two_tiles ? prompt_tc<T, 128, 2>(p, st) : prompt_tc<T, 128, 1>(p, st);
-}
-
 cudaError_t launch_prompt_tc(const PromptArgs& p, cudaStream_t st) {
-    return p.dtype == ENERGON_BF16 ? prompt_tc_t<__nv_bfloat16>(p, st) : prompt_tc_t<__half>(p, st);
+    if (p.dtype == ENERGON_BF16)
+        return p.head_dim == 64 ? prompt_tc<__nv_bfloat16, 64>(p, st) : prompt_tc<__nv_bfloat16, 128>(p, st);
+    return p.head_dim == 64 ? prompt_tc<__half, 64>(p, st) : prompt_tc<__half, 128>(p, st);
 }
 
 }  // namespace energon
