@@ -187,12 +187,12 @@ __global__ void __launch_bounds__(CW * 32, QT == 8 && sizeof(T) == 2 ? 3 : 2) ca
     let_next_grid_start();
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, cc = lane & 3;
-    const int split = blockIdx.x, b = blockIdx.z, P = c.page_len;
-    const int kvh = blockIdx.y / sp.q_tiles, qt = blockIdx.y % sp.q_tiles, group = a.n_heads / c.n_kv;
+    const int split = blockIdx.z, b = blockIdx.y, P = c.page_len;
+    const int kvh = blockIdx.x / sp.q_tiles, qt = blockIdx.x % sp.q_tiles, group = a.n_heads / c.n_kv;
     const int head0 = kvh * group + qt * QT, n_q = min(QT, group - qt * QT);
     bool bad;
     const int n = cached_len(c, b, bad);
-    if (bad && split == 0 && blockIdx.y == 0 && tid == 0) status_or(c.status, ENERGON_DEVICE_BAD_LENGTH);
+    if (bad && split == 0 && blockIdx.x == 0 && tid == 0) status_or(c.status, ENERGON_DEVICE_BAD_LENGTH);
     const int t_begin = split * sp.ws.chunk, t_end = min(n, t_begin + sp.ws.chunk);
     if (split > 0 && t_begin >= n) return;
 
@@ -678,7 +678,7 @@ static cudaError_t cache_attn(const CacheAttnArgs& a, cudaStream_t st) {
     sp.ws = attn_ws(a.ws, a.c.batch, a.c.max_len, a.n_heads, a.c.n_kv, HD, a.accumulate);
     sp.q_tiles = cdiv(a.n_heads / a.c.n_kv, QT);
     sp.timeout_ns = a.timeout_ns;
-    const dim3 grid(sp.ws.splits, a.c.n_kv * sp.q_tiles, a.c.batch);
+    const dim3 grid(a.c.n_kv * sp.q_tiles, a.c.batch, sp.ws.splits);
     cache_attn_kernel<T, HD, QT><<<grid, CW * 32, DCfg<HD>::SMEM, st>>>(tm_k, tm_v, a, sp);
     e = cudaGetLastError();
     FinishArgs f;
