@@ -30,9 +30,17 @@ struct PCfg {
 template <int HD>
 __device__ __forceinline__ void load_tile(float* dst, int ld, const float* __restrict__ src, int64_t ld_src, int rows,
                                           float mul) {
-    for (int e = threadIdx.x; e < PT * HD; e += 256) {
-        const int r = e / HD, d = e % HD;
-        dst[r * ld + d] = r < rows ? src[r * ld_src + d] * mul : 0.0f;
+    constexpr int PIECES = HD / 4, PER = PT * PIECES / 256;  // 16-byte pieces of a row, and per thread
+    float4 x[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = threadIdx.x + i * 256, r = e / PIECES;
+        x[i] = r < rows ? *reinterpret_cast<const float4*>(src + r * ld_src + e % PIECES * 4) : make_float4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = threadIdx.x + i * 256;
+        *reinterpret_cast<float4*>(dst + e / PIECES * ld + e % PIECES * 4) = make_float4(x[i].x * mul, x[i].y * mul, x[i].z * mul, x[i].w * mul);
     }
 }
 
