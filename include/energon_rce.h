@@ -485,6 +485,9 @@ ENERGON_API int energon_kv_append(const energon_kv_cache* cache, const int32_t* 
  *               its kv head, to cache->weight (required then).  Sequences may share pages
  *               (a common prefix); with accumulate the order in which they add to a shared
  *               page is not fixed.
+ * The products run on the tensor cores with the codes as fp16 numbers (exact) and fp32 sums.
+ * 16-bit queries enter as they are, fp32 queries to 22 bits; the probabilities, times their
+ * page's value scale, are rounded to fp16 for the product with the value codes (fp32: to 22 bits).
  * An empty sequence gives o = 0 and lse = -infinity.  Tokens of a bad page count as masked.
  *   workspace   energon_cache_attention_workspace_bytes bytes, 256-byte aligned; its contents
  *               need not be kept between calls.  Calls that may overlap need their own.
