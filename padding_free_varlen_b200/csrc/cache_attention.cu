@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(CW * 32, QT == 8 && sizeof(T) == 2 ? 3 : 2) ca
     __shared__ uint64_t bars[CW][STAGES];
     __shared__ float sh_m[CW][QT], sh_l[CW][QT];
     const CacheArgs& c = a.c;
-    if (stopped(c.status)) return;
+    if (block_stopped(c.status)) return;
     let_next_grid_start();
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, cc = lane & 3;
@@ -572,7 +572,7 @@ __global__ void __launch_bounds__(FIN) cache_finish_kernel(const FinishArgs fa) 
     const AttnWs& ws = fa.ws;
     const CacheArgs& c = a.c;
     wait_for_earlier_grid();
-    if (stopped(c.status)) return;
+    if (block_stopped(c.status)) return;
     const int b = blockIdx.z, kvh = blockIdx.y, group = ws.group, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     bool bad;
     const int n = cached_len(c, b, bad);

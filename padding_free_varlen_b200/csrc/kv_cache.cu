@@ -91,7 +91,7 @@ constexpr int APPEND_HELD = 128 * 128 / 8 / APPEND_THREADS;  // pieces of 8 elem
 template <typename T>
 __global__ void __launch_bounds__(APPEND_THREADS, sizeof(T) == 4 ? 2 : 4) kv_append_kernel(const AppendArgs a) {
     const CacheArgs& c = a.c;
-    if (stopped(c.status)) return;
+    if (block_stopped(c.status)) return;
     const int tid = threadIdx.x, P = c.page_len, d = c.head_dim, log_p = __ffs(P) - 1;
     if (blockIdx.x == 0 && blockIdx.y == 0 && tid < 32) {
         bool bad = false;
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const EvictAr
     __shared__ int counts[2][3][SEL_WARPS];
     __shared__ uint32_t taken[HELD][SEL_WARPS];
     let_next_grid_start();
-    if (stopped(c.status)) return;
+    if (block_stopped(c.status)) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int b = blockIdx.y, h = blockIdx.x, P = c.page_len, log_p = __ffs(P) - 1;
     const int item = b * c.n_kv + h;
@@ -460,7 +460,8 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const EvictAr
     }
 }
 
-// Codes times the token's factor, rounded.
+// Codes times the token's factor, rounded.  (Adding 1.5 * 2^23 to the product instead of converting it
+// gained nothing, and lost exactness where the two became one fused operation.)
 __device__ __forceinline__ uint4 scaled_codes(uint4 x, float f) {
     if (f == 1.0f) return x;
     uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -485,7 +486,7 @@ __device__ __forceinline__ uint4 scaled_codes(uint4 x, float f) {
 __global__ void __launch_bounds__(MOVE_THREADS) evict_move_kernel(const EvictArgs a) {
     const CacheArgs& c = a.c;
     wait_for_earlier_grid();
-    if (stopped(c.status)) return;
+    if (block_stopped(c.status)) return;
     const int tid = threadIdx.x, P = c.page_len, d = c.head_dim, log_p = __ffs(P) - 1;
     const int b = blockIdx.z, h = blockIdx.y, item = b * c.n_kv + h;
     const EvictWs ws = evict_ws(a.ws, c.batch * c.n_kv, a.budget);

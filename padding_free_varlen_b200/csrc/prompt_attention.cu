@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(256) prompt_simt_kernel(const PromptArgs p) {
     using C = PCfg<HD>;
     extern __shared__ float sm[];
     float *Q = sm, *K = Q + PT * C::LD, *V = K + PT * C::LD, *P = V + PT * HD;
-    if (stopped(p.status)) return;
+    if (block_stopped(p.status)) return;
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) check_rows(p.cu, p.batch, p.rows, p.status);
     int b, blk, start, n;
     auto count = [&](int i) {
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(256) key_weights_simt_kernel(const PromptArgs 
     extern __shared__ float sm[];
     float *Q = sm, *K = Q + PT * C::LD;
     __shared__ float part[16][PT];
-    if (stopped(p.status)) return;
+    if (block_stopped(p.status)) return;
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) check_rows(p.cu, p.batch, p.rows, p.status);
     int b, blk, start, n;
     auto count = [&](int i) {

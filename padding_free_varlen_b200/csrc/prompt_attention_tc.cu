@@ -218,7 +218,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     auto& odd = aux.odd;
     auto& first = aux.first;
     const PromptArgs& p = a.p;
-    if (stopped(p.status)) return;
+    if (block_stopped(p.status)) return;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
     uint8_t* ring_k = base + C::QT;

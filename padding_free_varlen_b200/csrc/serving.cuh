@@ -12,6 +12,10 @@ __device__ __forceinline__ bool stopped(const int32_t* st) {
     return st != nullptr && (*reinterpret_cast<const volatile int32_t*>(st) & ENERGON_DEVICE_TIMEOUT) != 0;
 }
 
+// The same for a whole block at once: another kernel may set the bit while this one starts, and warps that
+// meet at barriers, or take each other's counts, must not part.
+__device__ __forceinline__ bool block_stopped(const int32_t* st) { return __syncthreads_or(stopped(st)) != 0; }
+
 // Rows of sequence b of a packed batch; false (and n = 0) when they do not lie in [0, rows].
 __device__ __forceinline__ bool seq_rows(const int32_t* __restrict__ cu, int b, int rows, int& start, int& n) {
     start = cu[b];

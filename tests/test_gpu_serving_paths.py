@@ -260,6 +260,30 @@ def test_evict_long_contexts(n, kind, in_place):
     same(t, h)
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_between_two_codes(in_place):
+    """Ratios of scales that put the fp32 product of a code into the middle of two, where the exact
+    product lies beside it: every code times several such ratios."""
+    kv, d, P = 1, 64, 16
+    ratios = [1.0, 0.65, 0.55, 0.85, 0.35, 0.15, 0.95, 0.05, 0.7, 0.9, 0.1, 0.3]
+    n = len(ratios) * P
+    t = make(2 * len(ratios), kv, P, d, seed=1)
+    for i, r in enumerate(ratios):
+        t[2][i] = t[3][i] = float(np.float32(r) * np.float32(0.0173))
+    for c in t[:2]:
+        c[:len(ratios)] = ((torch.arange(P * d, device="cuda") * 7) % 255 - 127).to(torch.int8).view(1, 1, P, d)
+    t[4][:] = torch.rand(t[4].shape, device="cuda", generator=gen(2))
+    t[4][0] = 2                                          # the page of the largest scale is met by all
+    table = np.arange(len(ratios), dtype=np.int32)[None]
+    new_table = table if in_place else table + len(ratios)
+    for budget in (n - 1, 3 * P, P):
+        u = [x.clone() for x in t]
+        h = host(u)
+        want = ref.evict(h, table, [n], new_table, budget, 3)
+        assert call_evict(u, table, [n], new_table, budget, 3) == want
+        same(u, h)
+
+
 def test_calls_on_two_streams_at_once():
     """Two long calls of each operator, on two streams with outputs and workspaces of their own."""
     H, kv, d, P = 16, 4, 128, 64
