@@ -13,10 +13,10 @@
 // One block = 128 keys of one (sequence, kv head) and a part of the query heads that share them;
 // the blocks of a group form a cluster, whose first block adds their sums in a fixed order.  With few
 // queries per key (a window of up to 256) one block takes all heads: a block's start costs more than
-// the steps that the others would take from it (the last 64 queries of 8 prompts: 25 us, with clusters of
+// the steps that the others would take from it (the last 64 queries of 8 prompts: 22 us, with clusters of
 // 4 it took 68).
 //
-// One prompt of 4096 tokens, all queries, 32 heads of 128, 8 kv heads, fp16: 103 us, 665 TFLOP/s; its 268 million
+// One prompt of 4096 tokens, all queries, 32 heads of 128, 8 kv heads, fp16: 100 us, 687 TFLOP/s; its 268 million
 // exponentials alone would take the special function units 60 us.
 #include <cudaTypedefs.h>
 #include <math.h>
@@ -34,8 +34,8 @@ constexpr int BQ = 128;            // queries per step
 constexpr int BOX = 128 * 128;     // bytes of 128 rows x 64 columns of 16 bits
 constexpr int EXP_WARPS = 8;       // two threads per key, each with half of a step's queries
 constexpr int THREADS = EXP_WARPS * 32 + 96;  // and loader, products, sums
-// One pair of columns in four takes its exponentials from the FMA pipe (2^x by a polynomial): 103 us
-// on one prompt of 4096 tokens with 32 heads, against 110 us with none and 112 us with every second.
+// One pair of columns in four takes its exponentials from the FMA pipe (2^x by a polynomial): on
+// one prompt of 4096 tokens with 32 heads 6 % faster than none and 8 % faster than every second.
 constexpr int POLY = 8;
 constexpr float LOG2E = 1.4426950408889634f;
 
@@ -80,7 +80,7 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                       const KeyWeightArgs a) {
     using C = WCfg<HD>;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t k_full, q_full[2], q_empty[2], l_full[2], s_full[2], s_empty[2], drain;
+    __shared__ uint64_t k_full, q_full[2], q_empty[2], s_full[2], s_empty[2], drain;
     __shared__ uint32_t tmem_slot;
     __shared__ int dead;
     __shared__ __align__(16) float neg_lse[2][BQ];  // -lse in units of log2
@@ -90,6 +90,20 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     // blocks of a cluster share the item; items of all kv heads pass by before the next tile of keys
     const int64_t lin = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) / a.cluster;
     const int rank = blockIdx.x % a.cluster, kvh = (int)(lin % p.n_kv);
+    // What needs no length comes first: it runs under the loads of the lengths.
+    const bool stop = stopped(p.status);
+    if (warp == EXP_WARPS && lane == 0) {
+        mbar_init(&k_full, 1), mbar_init(&drain, 1);
+        for (int i = 0; i < 2; ++i)
+            mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 1), mbar_init(&s_full[i], 33), mbar_init(&s_empty[i], EXP_WARPS * 32);
+        dead = stop;  // the blocks of a cluster must not part: no early return
+        fence_mbar_init();
+        tma_prefetch_desc(&tm_k), tma_prefetch_desc(&tm_q);
+    }
+    if (warp == EXP_WARPS + 1) {
+        tmem_alloc(&tmem_slot, 2 * BQ);
+        tmem_relinquish();
+    }
     if (lin == 0 && rank == 0 && tid < 32 && !stopped(p.status)) check_rows(p.cu, p.batch, p.rows, p.status);
     int b, blk, start, n;
     auto count = [&](int i) {
@@ -97,7 +111,13 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         seq_rows(p.cu, i, p.rows, s, len);
         return (len + BK - 1) / BK;
     };
-    if (!find_item(p.batch, (int)(lin / p.n_kv), count, b, blk)) return;
+    if (!find_item(p.batch, (int)(lin / p.n_kv), count, b, blk)) {
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (warp == EXP_WARPS + 1) tmem_dealloc(__shfl_sync(0xffffffffu, tmem_slot, 0), 2 * BQ);
+        return;
+    }
     seq_rows(p.cu, b, p.rows, start, n);
     const int t0 = blk * BK, group = p.n_heads / p.n_kv, heads = group / a.cluster;
     const int head0 = kvh * group + rank * heads;
@@ -106,17 +126,18 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
 
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sq = base + C::TILE;
-    if (tid == 0) {
-        mbar_init(&k_full, 1), mbar_init(&drain, 1);
-        for (int i = 0; i < 2; ++i)
-            mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 1), mbar_init(&l_full[i], 32), mbar_init(&s_full[i], 1), mbar_init(&s_empty[i], EXP_WARPS * 32);
-        dead = stopped(p.status);  // the blocks of a cluster must not part: no early return
-        fence_mbar_init();
+    auto load_queries = [&](int x) {
+        mbar_arrive_expect_tx(&q_full[x & 1], C::TILE);
+        for (int h = 0; h < HD / 64; ++h)
+            tma_load_2d(sq + (x & 1) * C::TILE + h * BOX, &tm_q, &q_full[x & 1], (head0 + x / per_head) * HD + 64 * h,
+                        start + begin + x % per_head * BQ);
+    };
+    if (warp == EXP_WARPS && lane == 0 && !stop) {  // (this thread made the barriers)
+        mbar_arrive_expect_tx(&k_full, C::TILE);
+        for (int h = 0; h < HD / 64; ++h) tma_load_2d(base + h * BOX, &tm_k, &k_full, kvh * HD + 64 * h, start + t0);
+        for (int x = 0; x < min(steps, 2); ++x) load_queries(x);
     }
-    if (warp == EXP_WARPS) {
-        tmem_alloc(&tmem_slot, 2 * BQ);
-        tmem_relinquish();
-    }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -136,15 +157,10 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     } else if (warp == EXP_WARPS) {
         if (lane == 0) {
             // ---- loader
-            mbar_arrive_expect_tx(&k_full, C::TILE);
-            for (int h = 0; h < HD / 64; ++h) tma_load_2d(base + h * BOX, &tm_k, &k_full, kvh * HD + 64 * h, start + t0);
-            int x = 0;
+            int x = min(steps, 2);
             for (; x < steps; ++x) {
-                if (x >= 2 && !wait(&q_empty[x & 1], ((x >> 1) - 1) & 1)) break;
-                mbar_arrive_expect_tx(&q_full[x & 1], C::TILE);
-                for (int h = 0; h < HD / 64; ++h)
-                    tma_load_2d(sq + (x & 1) * C::TILE + h * BOX, &tm_q, &q_full[x & 1], (head0 + x / per_head) * HD + 64 * h,
-                                start + begin + x % per_head * BQ);
+                if (!wait(&q_empty[x & 1], ((x >> 1) - 1) & 1)) break;
+                load_queries(x);
             }
             // all copies have landed before the block ends, also where a wait ran out
             mbar_wait_bounded(&k_full, 0, nullptr, p.timeout_ns);
@@ -180,33 +196,30 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 const int s = s0 + i + lane;
                 neg_lse[x & 1][i + lane] = s < n ? -lse[s] * LOG2E : 0.0f;
             }
-            mbar_arrive(&l_full[x & 1]);
+            mbar_arrive(&s_full[x & 1]);  // with the products of this step
         }
     } else {
         // ---- exponentials
+        // (a thread's columns are the even or the odd groups of 32, so that few queries occupy both)
         const int half = warp >> 2, t = t0 + (tid & 127);
-        const uint32_t S = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * (BQ / 2);
+        const uint32_t S = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 32;
         const uint64_t c2 = two(a.c, a.c);
         uint64_t sum[2] = {two(0.0f, 0.0f), two(0.0f, 0.0f)};
         for (int x = 0; x < steps; ++x) {
             const int at = x & 1;
-            if (!wait_warp(&l_full[at], (x >> 1) & 1) || !wait_warp(&s_full[at], (x >> 1) & 1)) break;
+            if (!wait_warp(&s_full[at], (x >> 1) & 1)) break;
             tc_fence_after();
-            const int s0 = begin + x % per_head * BQ + half * (BQ / 2);
-            const bool edge = s0 < t0 + BK - 1 || s0 + BQ / 2 > n;
-            const int lo = t - s0, hi = n - s0;  // queries lo .. hi - 1 of these 64 see this key
-            if (hi > 0) {
-                uint32_t r[2][32];
-                tmem_ld_x32(S + at * BQ, r[0]);
-                tmem_ld_x32(S + at * BQ + 32, r[1]);
-                tmem_wait_ld_regs(r[0]);
-                tmem_wait_ld_regs(r[1]);
+            const int s0 = begin + x % per_head * BQ + half * 32;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float* l = &neg_lse[at][half * (BQ / 2) + 32 * h];
-                    if (edge) add_exponentials<true>(r[h], l, c2, lo - 32 * h, hi - 32 * h, sum);
-                    else add_exponentials<false>(r[h], l, c2, 0, 0, sum);
-                }
+            for (int h = 0; h < 2; ++h) {
+                const int s1 = s0 + 64 * h;  // queries s1 .. s1 + 31
+                if (s1 >= n) break;
+                uint32_t r[32];
+                tmem_ld_x32(S + at * BQ + 64 * h, r);
+                tmem_wait_ld_regs(r);
+                const float* l = &neg_lse[at][half * 32 + 64 * h];
+                if (s1 < t0 + BK - 1 || s1 + 32 > n) add_exponentials<true>(r, l, c2, t - s1, n - s1, sum);
+                else add_exponentials<false>(r, l, c2, 0, 0, sum);
             }
             tc_fence_before();
             mbar_arrive(&s_empty[at]);
@@ -218,7 +231,7 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == EXP_WARPS) tmem_dealloc(tmem, 2 * BQ);
+    if (warp == EXP_WARPS + 1) tmem_dealloc(tmem, 2 * BQ);
     if (tid == 0 && dead) status_or(p.status, ENERGON_DEVICE_TIMEOUT);
     if (tid < BK) part[0][tid] += part[1][tid];
     float w = tid < BK ? part[0][tid] : 0.0f;
