@@ -138,11 +138,17 @@ __device__ __forceinline__ uint32_t rest_f16(float a, float b, uint32_t hi) {
     const float2 h = unpack2<__half>(hi);
     return pack2<__half>(a - h.x, b - h.y);
 }
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int y, int z) {
+// The codes stream through L2 without displacing the scores, which are read again.
+__device__ __forceinline__ uint64_t streaming() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int y, int z, uint64_t policy) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "l"(policy)
         : "memory");
 }
 // Elements [0, N) of a row at p as floats.
@@ -260,6 +266,7 @@ __global__ void __launch_bounds__(CW * 32, QT == 8 && sizeof(T) == 2 ? 3 : 2) ca
     float v_most = 0.0f;  // largest value scale met: the unit of acc
     bool ok = true;
     uint8_t* mine = ring + warp * C::WARP;
+    const uint64_t policy = streaming();
     // Where this lane's pieces begin in a buffer: keys of token g (16-byte pieces 2c and 2c + 1, or c), values
     // of tokens 2c and 2c + 1 (piece g, or half of piece g / 2).  The swizzle repeats after 8 rows.
     const int k_at[2] = {g * HD + ((HD == 128 ? (2 * cc) ^ g : cc ^ ((g >> 1) & 3)) << 4), g * HD + (((2 * cc + 1) ^ g) << 4)};
@@ -319,17 +326,17 @@ __global__ void __launch_bounds__(CW * 32, QT == 8 && sizeof(T) == 2 ? 3 : 2) ca
                     if (live) mbar_arrive_expect_tx(bar, live * C::TILE);
                     else mbar_arrive(bar);
                     if (p0 >= 0) {
-                        tma_load_3d(k, &tm_k, bar, 0, 0, p0);
-                        tma_load_3d(v, &tm_v, bar, 0, 0, p0);
+                        tma_load_3d(k, &tm_k, bar, 0, 0, p0, policy);
+                        tma_load_3d(v, &tm_v, bar, 0, 0, p0, policy);
                     }
                     if (p1 >= 0) {
-                        tma_load_3d(k + C::TILE / 2, &tm_k, bar, 0, 0, p1);
-                        tma_load_3d(v + C::TILE / 2, &tm_v, bar, 0, 0, p1);
+                        tma_load_3d(k + C::TILE / 2, &tm_k, bar, 0, 0, p1, policy);
+                        tma_load_3d(v + C::TILE / 2, &tm_v, bar, 0, 0, p1, policy);
                     }
                 } else if (p0 >= 0) {
                     mbar_arrive_expect_tx(bar, 2 * C::TILE);
-                    tma_load_3d(k, &tm_k, bar, 0, t & (P - 1), p0);
-                    tma_load_3d(v, &tm_v, bar, 0, t & (P - 1), p0);
+                    tma_load_3d(k, &tm_k, bar, 0, t & (P - 1), p0, policy);
+                    tma_load_3d(v, &tm_v, bar, 0, t & (P - 1), p0, policy);
                 } else {
                     mbar_arrive(bar);
                 }
