@@ -19,10 +19,11 @@
 // splits of a long sequence by a second kernel, which also adds the weights from the scores that the
 // first one left (they need the sums over all splits).
 //
-// 64 sequences of 1 to 8192 tokens (261 thousand in all), 64 heads of 128, 8 kv heads, bf16: 107 us without
-// weights, 5.0 TB/s (0.77 of the measured copy rate), 136 us with them.  What bounds it: turning
+// 64 sequences of 1 to 8192 tokens (261 thousand in all), 64 heads of 128, 8 kv heads, bf16: 104 us without
+// weights, 5.2 TB/s (0.79 of the measured copy rate), 134 us with them.  What bounds it: turning
 // a step's 8 KB of codes into fp16 takes 350 of the about 640 instructions of a step and warp (3 warps per
-// scheduler, 0.56 instructions a cycle); the scores cost 63 MB written and read.  Tried: four blocks per SM with
+// scheduler, 0.56 instructions a cycle); the scores cost 17 us to write and 20 us in the
+// second kernel, although they stay in L2.  Tried: four blocks per SM with
 // one buffer for V (143 us), splits of 512, 1024 and 4096 tokens (159, 140, 152 us) instead of 2048, queries
 // as the rows of the first product (half of a tile empty, 156 us).
 #include <cudaTypedefs.h>

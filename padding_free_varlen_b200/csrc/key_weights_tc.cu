@@ -74,7 +74,8 @@ struct KeyWeightArgs {
     int cluster;  // blocks that share the heads of a group
 };
 
-template <typename T, int HD>
+// QW: queries of a head in a step.  A window of at most 64 (32) leaves room for two (four) heads in it.
+template <typename T, int HD, int QW>
 __global__ void __launch_bounds__(THREADS, 2)
 key_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const KeyWeightArgs a) {
@@ -122,15 +123,22 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     const int t0 = blk * BK, group = p.n_heads / p.n_kv, heads = group / a.cluster;
     const int head0 = kvh * group + rank * heads;
     const int begin = max(t0, n - min(p.window, n));  // first query that counts for these keys
-    const int per_head = (n - begin + BQ - 1) / BQ, steps = per_head * heads;
+    constexpr int PACK = BQ / QW;                               // heads of a step
+    const int per_head = PACK > 1 ? 1 : (n - begin + BQ - 1) / BQ;  // (PACK > 1: n - begin <= window <= QW)
+    const int steps = PACK > 1 ? (heads + PACK - 1) / PACK : per_head * heads;
+    // column c of step x: head `head_of` of this block (may be behind the last), query `query_of`
+    auto head_of = [&](int x, int c) { return x / per_head * PACK + c / QW; };
+    auto query_of = [&](int x, int c) { return begin + x % per_head * BQ + c % QW; };
 
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sq = base + C::TILE;
     auto load_queries = [&](int x) {
-        mbar_arrive_expect_tx(&q_full[x & 1], C::TILE);
-        for (int h = 0; h < HD / 64; ++h)
-            tma_load_2d(sq + (x & 1) * C::TILE + h * BOX, &tm_q, &q_full[x & 1], (head0 + x / per_head) * HD + 64 * h,
-                        start + begin + x % per_head * BQ);
+        const int live = min(PACK, heads - head_of(x, 0));
+        mbar_arrive_expect_tx(&q_full[x & 1], C::TILE / PACK * live);
+        for (int i = 0; i < live; ++i)
+            for (int h = 0; h < HD / 64; ++h)
+                tma_load_2d(sq + (x & 1) * C::TILE + h * BOX + i * QW * 128, &tm_q, &q_full[x & 1],
+                            (head0 + head_of(x, i * QW)) * HD + 64 * h, start + query_of(x, 0));
     };
     if (warp == EXP_WARPS && lane == 0 && !stop) {  // (this thread made the barriers)
         mbar_arrive_expect_tx(&k_full, C::TILE);
@@ -189,12 +197,10 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         // ---- sums of the queries
         for (int x = 0; x < steps; ++x) {
             if (x >= 2 && !wait(&s_empty[x & 1], ((x >> 1) - 1) & 1)) break;
-            const float* lse = p.lse + (int64_t)(head0 + x / per_head) * p.rows + start;
-            const int s0 = begin + x % per_head * BQ;
 #pragma unroll
             for (int i = 0; i < BQ; i += 32) {
-                const int s = s0 + i + lane;
-                neg_lse[x & 1][i + lane] = s < n ? -lse[s] * LOG2E : 0.0f;
+                const int head = head_of(x, i), s = query_of(x, i) + lane;  // (32 columns are of one head)
+                neg_lse[x & 1][i + lane] = head < heads && s < n ? -p.lse[(int64_t)(head0 + head) * p.rows + start + s] * LOG2E : 0.0f;
             }
             mbar_arrive(&s_full[x & 1]);  // with the products of this step
         }
@@ -209,11 +215,10 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             const int at = x & 1;
             if (!wait_warp(&s_full[at], (x >> 1) & 1)) break;
             tc_fence_after();
-            const int s0 = begin + x % per_head * BQ + half * 32;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int s1 = s0 + 64 * h;  // queries s1 .. s1 + 31
-                if (s1 >= n) break;
+                const int s1 = query_of(x, half * 32 + 64 * h);  // queries s1 .. s1 + 31
+                if (s1 >= n || head_of(x, half * 32 + 64 * h) >= heads) continue;
                 uint32_t r[32];
                 tmem_ld_x32(S + at * BQ + 64 * h, r);
                 tmem_wait_ld_regs(r);
@@ -254,13 +259,13 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     if (rank == 0 && good && tid < BK && t0 + tid < n) p.weights[(int64_t)kvh * p.rows + start + t0 + tid] = w;
 }
 
-template <typename T, int HD>
+template <typename T, int HD, int QW>
 static cudaError_t key_weights_tc(const PromptArgs& p, cudaStream_t st) {
     using C = WCfg<HD>;
     CUtensorMap q, k;
-    cudaError_t e = rows_map(&q, p.dtype, p.q, (int64_t)p.n_heads * HD, p.rows, p.ld_q, BQ);
+    cudaError_t e = rows_map(&q, p.dtype, p.q, (int64_t)p.n_heads * HD, p.rows, p.ld_q, QW);
     if (e == cudaSuccess) e = rows_map(&k, p.dtype, p.k, (int64_t)p.n_kv * HD, p.rows, p.ld_k, BK);
-    if (e == cudaSuccess) e = prepare_smem((const void*)key_weights_tc_kernel<T, HD>, C::SMEM);
+    if (e == cudaSuccess) e = prepare_smem((const void*)key_weights_tc_kernel<T, HD, QW>, C::SMEM);
     if (e != cudaSuccess) return e;
     KeyWeightArgs a;
     a.p = p;
@@ -277,13 +282,22 @@ static cudaError_t key_weights_tc(const PromptArgs& p, cudaStream_t st) {
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = a.cluster, at[0].val.clusterDim.y = 1, at[0].val.clusterDim.z = 1;
     cfg.attrs = at, cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, key_weights_tc_kernel<T, HD>, q, k, a);
+    return cudaLaunchKernelEx(&cfg, key_weights_tc_kernel<T, HD, QW>, q, k, a);
+}
+
+template <typename T, int HD>
+static cudaError_t key_weights_tc_w(const PromptArgs& p, cudaStream_t st) {
+    // heads share a step where the window leaves room: on the last 64 queries of 8 prompts PACKED us instead of 22
+    const bool share = p.n_heads > p.n_kv;
+    if (share && p.window <= 32) return key_weights_tc<T, HD, 32>(p, st);
+    if (share && p.window <= 64) return key_weights_tc<T, HD, 64>(p, st);
+    return key_weights_tc<T, HD, 128>(p, st);
 }
 
 cudaError_t launch_key_weights_tc(const PromptArgs& p, cudaStream_t st) {
     if (p.dtype == ENERGON_BF16)
-        return p.head_dim == 64 ? key_weights_tc<__nv_bfloat16, 64>(p, st) : key_weights_tc<__nv_bfloat16, 128>(p, st);
-    return p.head_dim == 64 ? key_weights_tc<__half, 64>(p, st) : key_weights_tc<__half, 128>(p, st);
+        return p.head_dim == 64 ? key_weights_tc_w<__nv_bfloat16, 64>(p, st) : key_weights_tc_w<__nv_bfloat16, 128>(p, st);
+    return p.head_dim == 64 ? key_weights_tc_w<__half, 64>(p, st) : key_weights_tc_w<__half, 128>(p, st);
 }
 
 }  // namespace energon
