@@ -13,8 +13,8 @@
 // One block = 128 keys of one (sequence, kv head) and a part of the query heads that share them;
 // the blocks of a group form a cluster, whose first block adds their sums in a fixed order.  With few
 // queries per key (a window of up to 256) one block takes all heads: a block's start costs more than
-// the steps that the others would take from it (the last 64 queries of 8 prompts: 22 us, with clusters of
-// 4 it took 68).
+// the steps that the others would take from it (the last 64 queries of 8 prompts: 18.6 us, with
+// clusters of 4, and a head per step, it took 68).
 //
 // One prompt of 4096 tokens, all queries, 32 heads of 128, 8 kv heads, fp16: 100 us, 687 TFLOP/s; its 268 million
 // exponentials alone would take the special function units 60 us.
@@ -127,8 +127,8 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     const int per_head = PACK > 1 ? 1 : (n - begin + BQ - 1) / BQ;  // (PACK > 1: n - begin <= window <= QW)
     const int steps = PACK > 1 ? (heads + PACK - 1) / PACK : per_head * heads;
     // column c of step x: head `head_of` of this block (may be behind the last), query `query_of`
-    auto head_of = [&](int x, int c) { return x / per_head * PACK + c / QW; };
-    auto query_of = [&](int x, int c) { return begin + x % per_head * BQ + c % QW; };
+    auto head_of = [&](int x, int c) { return PACK > 1 ? x * PACK + c / QW : x / per_head; };
+    auto query_of = [&](int x, int c) { return PACK > 1 ? begin + c % QW : begin + x % per_head * BQ + c; };
 
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sq = base + C::TILE;
@@ -215,10 +215,11 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             const int at = x & 1;
             if (!wait_warp(&s_full[at], (x >> 1) & 1)) break;
             tc_fence_after();
+            const int s0 = query_of(x, half * 32);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int s1 = query_of(x, half * 32 + 64 * h);  // queries s1 .. s1 + 31
-                if (s1 >= n || head_of(x, half * 32 + 64 * h) >= heads) continue;
+                const int s1 = PACK > 1 ? query_of(x, half * 32 + 64 * h) : s0 + 64 * h;  // queries s1 .. s1 + 31
+                if (s1 >= n || (PACK > 1 && head_of(x, half * 32 + 64 * h) >= heads)) continue;
                 uint32_t r[32];
                 tmem_ld_x32(S + at * BQ + 64 * h, r);
                 tmem_wait_ld_regs(r);
@@ -287,7 +288,8 @@ static cudaError_t key_weights_tc(const PromptArgs& p, cudaStream_t st) {
 
 template <typename T, int HD>
 static cudaError_t key_weights_tc_w(const PromptArgs& p, cudaStream_t st) {
-    // heads share a step where the window leaves room: on the last 64 queries of 8 prompts PACKED us instead of 22
+    // heads share a step where the window leaves room: on the last 64 queries of 8 prompts 18.6 us
+    // instead of 22.3, on the last 32 14.9
     const bool share = p.n_heads > p.n_kv;
     if (share && p.window <= 32) return key_weights_tc<T, HD, 32>(p, st);
     if (share && p.window <= 64) return key_weights_tc<T, HD, 64>(p, st);

@@ -122,7 +122,7 @@ def test_prompt_values_not_finite_in_many_items(dt):
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
 @pytest.mark.parametrize("H,kv,d", [(14, 2, 128), (5, 1, 64), (16, 1, 128), (22, 2, 64), (12, 12, 128)])
-@pytest.mark.parametrize("window", [37, 300, 1 << 30])
+@pytest.mark.parametrize("window", [1, 32, 37, 64, 65, 300, 1 << 30])
 def test_key_weights_groups(dt, H, kv, d, window):
     """Groups of 1, 5, 7, 8, 11 and 16 heads, shared by clusters of every size; steps over several tiles."""
     lens = [700, 0, 129, 1, 384, 511]
