@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(256) prompt_simt_kernel(const PromptArgs p) {
         load_tile<HD>(K, C::LD, k + (int64_t)k0 * p.ld_k, p.ld_k, n - k0, 1.0f);
         load_tile<HD>(V, HD, v + (int64_t)k0 * p.ld_v, p.ld_v, n - k0, 1.0f);
         __syncthreads();
+        if (q0 + (ty & ~1) * 4 >= n) continue;  // none of this warp's 8 queries is there
         float x[4][4];
         tile_scores<HD>(Q, K, ty, tx, x);
         const bool diag = k0 == q0;  // the only tile with keys after a query
@@ -214,6 +215,7 @@ __global__ void __launch_bounds__(256) key_weights_simt_kernel(const PromptArgs 
             load_tile<HD>(Q, C::LD, static_cast<const float*>(p.q) + (int64_t)(start + s0) * p.ld_q + (int64_t)head * HD,
                              p.ld_q, n - s0, p.scale * LOG2E);
             __syncthreads();
+            if (s0 + (ty & ~1) * 4 >= n) continue;  // none of this warp's 8 queries is there
             float x[4][4];
             tile_scores<HD>(Q, K, ty, tx, x);
 #pragma unroll
