@@ -351,7 +351,8 @@ __global__ void __launch_bounds__(CW * 32, QT == 8 && sizeof(T) == 2 ? 3 : 2) ca
             if (!ok) {
                 // let the copies that are still in flight land before the block may end
                 for (int j = i; j < min(i + STAGES, now); ++j)
-                    mbar_wait_bounded(&bars[warp][(used + j) % STAGES], ((used + j) / STAGES) & 1, nullptr, sp.timeout_ns);
+                    mbar_wait_bounded(&bars[warp][(used + j) % STAGES], ((used + j) / STAGES) & 1, nullptr,
+                                      landing_limit(sp.timeout_ns));
                 break;
             }
             const uint8_t* buf = mine + at * 2 * C::TILE;

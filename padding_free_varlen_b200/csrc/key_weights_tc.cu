@@ -171,8 +171,8 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 load_queries(x);
             }
             // all copies have landed before the block ends, also where a wait ran out
-            mbar_wait_bounded(&k_full, 0, nullptr, p.timeout_ns);
-            for (int y = max(0, x - 2); y < x; ++y) mbar_wait_bounded(&q_full[y & 1], (y >> 1) & 1, nullptr, p.timeout_ns);
+            mbar_wait_bounded(&k_full, 0, nullptr, landing_limit(p.timeout_ns));
+            for (int y = max(0, x - 2); y < x; ++y) mbar_wait_bounded(&q_full[y & 1], (y >> 1) & 1, nullptr, landing_limit(p.timeout_ns));
         }
     } else if (warp == EXP_WARPS + 1) {
         // ---- products: the whole warp follows, one lane issues
@@ -192,7 +192,7 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             }
         }
         if (elect_one()) umma_commit(&drain);  // all products are done before the block ends
-        mbar_wait_bounded(&drain, 0, nullptr, p.timeout_ns);
+        mbar_wait_bounded(&drain, 0, nullptr, landing_limit(p.timeout_ns));
     } else if (warp == EXP_WARPS + 2) {
         // ---- sums of the queries
         for (int x = 0; x < steps; ++x) {

@@ -328,7 +328,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 ++k;
             }
             // the answer is waited for in any case: it must not land in a block that has ended
-            const bool answered = __all_sync(0xffffffffu, mbar_wait_bounded(&answer_bar, asked & 1, nullptr, p.timeout_ns)) != 0;
+            const bool answered = __all_sync(0xffffffffu, mbar_wait_bounded(&answer_bar, asked & 1, nullptr, landing_limit(p.timeout_ns))) != 0;
             ++asked;
             if (!answered) *reinterpret_cast<volatile int*>(&dead) = 1, ok = false;
             more = answered && next_block(&answer, x, y);
@@ -337,11 +337,11 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
         if (ok) announce(make_int4(0, 0, 0, 0));
         // All copies have landed before the block ends, also where a wait ran out.
-        if (k > 0) mbar_wait_bounded(&q_full, (k - 1) & 1, nullptr, p.timeout_ns);
-        for (int g = max(0, nk - C::RING); g < nk; ++g) mbar_wait_bounded(&k_full[g % C::RING], (g / C::RING) & 1, nullptr, p.timeout_ns);
-        for (int g = max(0, nv - C::RING); g < nv; ++g) mbar_wait_bounded(&v_full[g % C::RING], (g / C::RING) & 1, nullptr, p.timeout_ns);
+        if (k > 0) mbar_wait_bounded(&q_full, (k - 1) & 1, nullptr, landing_limit(p.timeout_ns));
+        for (int g = max(0, nk - C::RING); g < nk; ++g) mbar_wait_bounded(&k_full[g % C::RING], (g / C::RING) & 1, nullptr, landing_limit(p.timeout_ns));
+        for (int g = max(0, nv - C::RING); g < nv; ++g) mbar_wait_bounded(&v_full[g % C::RING], (g / C::RING) & 1, nullptr, landing_limit(p.timeout_ns));
         for (int i = 0; i < C::RING; ++i)  // (an unused one passes: the phase before its first counts as done)
-            mbar_wait_bounded(&v_in[i], (ins >> i & 1) ^ 1, nullptr, p.timeout_ns);
+            mbar_wait_bounded(&v_in[i], (ins >> i & 1) ^ 1, nullptr, landing_limit(p.timeout_ns));
     } else if (warp == SOFT + 1) {
         // ---- products: the whole warp follows, one lane issues.  The scores run up to two blocks
         // ahead of the products with V, over the ends of items; whichever of the two can go on does (the
@@ -424,7 +424,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
         }
         if (elect_one()) umma_commit(&drain);  // all products are done before the block ends
-        mbar_wait_bounded(&drain, 0, nullptr, p.timeout_ns);
+        mbar_wait_bounded(&drain, 0, nullptr, landing_limit(p.timeout_ns));
     } else if (warp > SOFT + 1) {
         // ---- scan of V
         constexpr uint32_t INF = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;

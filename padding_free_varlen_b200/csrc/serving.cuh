@@ -100,6 +100,10 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 
+// Limit of the waits for copies and products that are in flight when a block ends: they must not land
+// in the shared memory of the next block, however short the limit that a caller set for other waits.
+__device__ __forceinline__ uint64_t landing_limit(uint64_t timeout_ns) { return timeout_ns > 1000000000ull ? timeout_ns : 1000000000ull; }
+
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ uint64_t two(float lo, float hi) {
     uint64_t r;
