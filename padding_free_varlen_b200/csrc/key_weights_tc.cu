@@ -63,7 +63,7 @@ __device__ __forceinline__ void add_exponentials(const uint32_t* r, const float*
             if (e + 3 < lo || e + 3 >= hi) v.y = -INFINITY;
         }
         sum[0] = add2(sum[0], two(exp2_fast(u.x), exp2_fast(u.y)));
-        v = e % POLY == 0 ? exp2_poly<5>(v) : make_float2(exp2_fast(v.x), exp2_fast(v.y));
+        v = e % POLY == 0 ? exp2_poly(v) : make_float2(exp2_fast(v.x), exp2_fast(v.y));
         sum[1] = add2(sum[1], two(v.x, v.y));
     }
 }

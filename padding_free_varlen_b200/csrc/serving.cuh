@@ -143,29 +143,20 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 
 // 2^x of a pair without the special function unit (16 results per cycle and SM, where the FMA pipe
-// makes 128 operations): x = j + f with j whole and |f| <= 1/2, 2^f by a polynomial with constant
-// term 1 fitted for the smallest relative error (DEG 4: 2.9e-6, DEG 5: 1.7e-7), times 2^j from j's
-// bits.  x <= 126; below -126 the result is 0 or next to it; NaN stays NaN.
-template <int DEG>
+// makes 128 operations): x = j + f with j whole and |f| <= 1/2, 2^f by a polynomial of degree 5 with
+// constant term 1 fitted for the smallest relative error (1.7e-7), times 2^j from j's bits.
+// x <= 126; below -126 the result is 0 or next to it; NaN stays NaN.
 __device__ __forceinline__ float2 exp2_poly(float2 x) {
-    static_assert(DEG == 4 || DEG == 5, "");
     constexpr float MAGIC = 12582912.0f;  // 1.5 * 2^23: adding it rounds to a whole number
     asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.x) : "f"(-127.0f));
     asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.y) : "f"(-127.0f));
     const uint64_t t = two(x.x, x.y);
     const uint64_t r = add2(t, two(MAGIC, MAGIC));
     const uint64_t f = fma2(add2(r, two(-MAGIC, -MAGIC)), two(-1.0f, -1.0f), t);
-    uint64_t y;
-    if constexpr (DEG == 4) {
-        y = fma2(f, two(0.009582851082f, 0.009582851082f), two(0.055906426162f, 0.055906426162f));
-        y = fma2(y, f, two(0.240240991116f, 0.240240991116f));
-        y = fma2(y, f, two(0.693124175072f, 0.693124175072f));
-    } else {
-        y = fma2(f, two(0.001326472033f, 0.001326472033f), two(0.009671512991f, 0.009671512991f));
-        y = fma2(y, f, two(0.055507339537f, 0.055507339537f));
-        y = fma2(y, f, two(0.240222424269f, 0.240222424269f));
-        y = fma2(y, f, two(0.693147003651f, 0.693147003651f));
-    }
+    uint64_t y = fma2(f, two(0.001326472033f, 0.001326472033f), two(0.009671512991f, 0.009671512991f));
+    y = fma2(y, f, two(0.055507339537f, 0.055507339537f));
+    y = fma2(y, f, two(0.240222424269f, 0.240222424269f));
+    y = fma2(y, f, two(0.693147003651f, 0.693147003651f));
     y = fma2(y, f, two(1.0f, 1.0f));
     // the low bits of r are those of j
     const float2 j = one_by_one(r);
