@@ -488,7 +488,8 @@ ENERGON_API int energon_kv_append(const energon_kv_cache* cache, const int32_t* 
  * The products run on the tensor cores with the codes as fp16 numbers (exact) and fp32 sums.
  * 16-bit queries enter as they are, fp32 queries to 22 bits; the probabilities, times their
  * page's value scale, are rounded to fp16 for the product with the value codes (fp32: to 22 bits).
- * An empty sequence gives o = 0 and lse = -infinity.  Tokens of a bad page count as masked.
+ * An empty sequence gives o = 0 and lse = -infinity.  Tokens of a bad page count as masked.  A query
+ * element that is not finite gives NaN in its head's o, lse and added weights.
  *   workspace   energon_cache_attention_workspace_bytes bytes, 256-byte aligned; its contents
  *               need not be kept between calls.  Calls that may overlap need their own.
  */

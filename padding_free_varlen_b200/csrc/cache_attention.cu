@@ -240,8 +240,9 @@ __global__ void __launch_bounds__(CW * 32, QT == 8 && sizeof(T) == 2 ? 3 : 2) ca
         const int e = most > 0.0f ? max((int)(__float_as_uint(most) >> 23), 1) - 126 : 0;
         const float q_unit = ldexpf(a.scale * LOG2E, e - 15);
         qs[r][0] = __shfl_sync(0xffffffffu, q_unit, 8 * cc), qs[r][1] = __shfl_sync(0xffffffffu, q_unit, 8 * cc + 4);
-        // 2^(15 - e) in two factors: alone it may lie outside the range of fp32
-        const float up0 = power_of_two((15 - e) / 2), up1 = power_of_two(15 - e - (15 - e) / 2);
+        // 2^(15 - e) in two factors: alone it may lie outside the range of fp32.  An infinite element makes all
+        // scores infinite or NaN; the softmax of such a row is NaN, also where all of them are -infinity.
+        const float up0 = most < INFINITY ? power_of_two((15 - e) / 2) : NAN, up1 = power_of_two(15 - e - (15 - e) / 2);
 #pragma unroll
         for (int s = 0; s < KS; ++s)
 #pragma unroll
@@ -311,8 +312,7 @@ __global__ void __launch_bounds__(CW * 32, QT == 8 && sizeof(T) == 2 ? 3 : 2) ca
                     for (int e = 0; e < 4; ++e) acc[r][i][e] *= by;
         }
         v_most = v_new;
-        vs[0] = v_most > 0.0f ? vs[0] / v_most * P_UP : 0.0f;
-        vs[1] = v_most > 0.0f ? vs[1] / v_most * P_UP : 0.0f;
+        if (v_most > 0.0f) vs[0] = vs[0] / v_most * P_UP, vs[1] = vs[1] / v_most * P_UP;  // (else 0, or NaN)
 
         auto fetch = [&](int i) {
             const int p0 = __shfl_sync(0xffffffffu, tile[0], i), p1 = __shfl_sync(0xffffffffu, tile[1], i);
@@ -533,7 +533,8 @@ __global__ void __launch_bounds__(CW * 32, QT == 8 && sizeof(T) == 2 ? 3 : 2) ca
 #pragma unroll
         for (int w = 0; w < CW; ++w) {
             const float mw = sh_m[w][q];
-            sum += mw == -INFINITY ? 0.0f : sh_l[w][q] * exp2_fast(mw - top);
+            // where no maximum was met the sum is 0, or NaN: a NaN score counts in no maximum
+            sum += mw == -INFINITY ? sh_l[w][q] : sh_l[w][q] * exp2_fast(mw - top);
             const float4 y = *reinterpret_cast<const float4*>(out + (w * QT + q) * LD + d);
             o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
         }
@@ -571,7 +572,7 @@ __device__ __forceinline__ float2 join_sums(const AttnWs& ws, int64_t row, int l
         const float2 ml = ws.ml[row * ws.splits + s];
         const float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - top);
         if (f) f[s] = w;
-        l += ml.x == -INFINITY ? 0.0f : ml.y * w;
+        l += ml.x == -INFINITY ? ml.y : ml.y * w;  // (0, or NaN)
     }
     return make_float2(top, warp_sum(l));
 }
