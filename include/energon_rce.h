@@ -400,7 +400,9 @@ ENERGON_API int energon_sched_fifo(const energon_request* reqs, int n, int max_b
  *     o_j(s) = sum_{t <= s} softmax_t(scale q_j(s) . k(t)) v(t)
  *   cu_seqlens  [batch + 1] int32 device, as energon_rce_offsets writes it
  *   rows        rows allocated in q, k, v and o.  A sequence whose rows do not lie in
- *               [0, rows] is skipped and sets ENERGON_DEVICE_BAD_LENGTH.
+ *               [0, rows], or one of whose rows lies between the first and the last row of
+ *               the sequences before it (the offsets step back), is skipped and sets
+ *               ENERGON_DEVICE_BAD_LENGTH.
  *   o           rows of no sequence are not written
  *   lse         optional [n_heads, rows] fp32: log sum_{t <= s} exp(scale q . k)
  * fp32: CUDA cores, fp32 products.  fp16 / bf16: tensor cores, fp32 sums; the
@@ -468,7 +470,8 @@ typedef struct {
  * the normal fp32 range are held as 0.  NaN is stored as 0 and an infinity as +-127, neither
  * counts for the scale, and ENERGON_DEVICE_NONFINITE is set.
  * Otherwise slots that receive no token keep their codes.  A sequence with more new tokens
- * than its length sets ENERGON_DEVICE_BAD_LENGTH and is skipped.  A page must belong to one sequence.
+ * than its length sets ENERGON_DEVICE_BAD_LENGTH and is skipped, and so is one whose rows
+ * energon_prompt_attention would skip.  A page must belong to one sequence.
  */
 ENERGON_API int energon_kv_append(const energon_kv_cache* cache, const int32_t* page_table, int max_pages,
                                   const int32_t* cache_lens, const void* k, int64_t ld_k, const void* v, int64_t ld_v,

@@ -85,12 +85,8 @@ __global__ void __launch_bounds__(256) prompt_simt_kernel(const PromptArgs p) {
     if (block_stopped(p.status)) return;
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) check_rows(p.cu, p.batch, p.rows, p.status);
     int b, blk, start, n;
-    auto count = [&](int i) {
-        int s, len;
-        seq_rows(p.cu, i, p.rows, s, len);
-        return (len + PT - 1) / PT;
-    };
-    if (!find_item(p.batch, blockIdx.x, count, b, blk)) return;
+    auto count = [](int, int len) { return (len + PT - 1) / PT; };
+    if (!find_item(p.cu, p.batch, p.rows, blockIdx.x, count, b, blk)) return;
     seq_rows(p.cu, b, p.rows, start, n);
     const int head = blockIdx.y, kvh = head / (p.n_heads / p.n_kv), q0 = blk * PT;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
@@ -195,12 +191,8 @@ __global__ void __launch_bounds__(256) key_weights_simt_kernel(const PromptArgs 
     if (block_stopped(p.status)) return;
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) check_rows(p.cu, p.batch, p.rows, p.status);
     int b, blk, start, n;
-    auto count = [&](int i) {
-        int s, len;
-        seq_rows(p.cu, i, p.rows, s, len);
-        return (len + PT - 1) / PT;
-    };
-    if (!find_item(p.batch, blockIdx.x, count, b, blk)) return;
+    auto count = [](int, int len) { return (len + PT - 1) / PT; };
+    if (!find_item(p.cu, p.batch, p.rows, blockIdx.x, count, b, blk)) return;
     seq_rows(p.cu, b, p.rows, start, n);
     const int kvh = blockIdx.y, group = p.n_heads / p.n_kv, t0 = blk * PT;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;

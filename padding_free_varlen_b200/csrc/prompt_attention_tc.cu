@@ -286,12 +286,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             const int64_t lin = (int64_t)y * gridDim.x + x;  // heads pass by first
             if (lin == 0) check_rows(p.cu, p.batch, p.rows, p.status);
             int b, blk;
-            auto count = [&](int i) {
-                int s, len;
-                seq_rows(p.cu, i, p.rows, s, len);
-                return (len + BM - 1) / BM;
-            };
-            if (find_item(p.batch, (int)(lin / p.n_heads), count, b, blk)) {
+            auto count = [](int, int len) { return (len + BM - 1) / BM; };
+            if (find_item(p.cu, p.batch, p.rows, (int)(lin / p.n_heads), count, b, blk)) {
                 seq_rows(p.cu, b, p.rows, it.start, it.n);
                 it.blk = (it.n + BM - 1) / BM - 1 - blk;  // the longest rows first
                 it.head = (int)(lin % p.n_heads);

@@ -26,15 +26,54 @@ __device__ __forceinline__ bool seq_rows(const int32_t* __restrict__ cu, int b, 
     return false;
 }
 
-// Work item `item` of a batch in which sequence b has count(b) items (>= 0): the sequence and
-// the item's index inside it.  Every warp computes it for itself, 32 sequences at a time; the
-// result is the same in every thread.  False when there are fewer items.
+// Passes over the sequences of a packed batch, 32 at a time (a lane each), and tells which are good: rows in
+// [0, rows], none of them between the first and the last row of the sequences before.  Good sequences then
+// share no row, so that none is written twice and the launches' bounds on the work hold whatever the
+// offsets are.  While all offsets ascend that costs one vote; behind the first sequence that is not good the rows
+// passed so far are followed by scans.
+struct RowWalk {
+    int lo = 0x7fffffff, hi = -1;  // first and last + 1 of the rows passed (where `straight` is false)
+    bool straight = true;
+    // Sequence base + lane: its rows; false where it is not good (n = 0 then), true behind the last one (n = 0).
+    __device__ __forceinline__ bool step(const int32_t* __restrict__ cu, int batch, int base, int rows, int& start, int& n) {
+        constexpr unsigned ALL = 0xffffffffu;
+        const int lane = threadIdx.x & 31;
+        start = n = 0;
+        const bool inside = base + lane >= batch || seq_rows(cu, base + lane, rows, start, n);
+        if (straight) {
+            if (__all_sync(ALL, inside)) return true;
+            straight = false;
+            const int first = cu[0], now = cu[base];
+            if (first < now) lo = first, hi = now;
+        }
+        int a = n > 0 ? start : 0x7fffffff, z = n > 0 ? start + n : -1;  // of this sequence and those before
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(ALL, a, o), y = __shfl_up_sync(ALL, z, o);
+            if (lane >= o) a = min(a, x), z = max(z, y);
+        }
+        a = min(a, lo), z = max(z, hi);
+        int before_lo = __shfl_up_sync(ALL, a, 1), before_hi = __shfl_up_sync(ALL, z, 1);
+        if (lane == 0) before_lo = lo, before_hi = hi;
+        lo = __shfl_sync(ALL, a, 31), hi = __shfl_sync(ALL, z, 31);
+        const bool good = inside && (n == 0 || start >= before_hi || start + n <= before_lo);
+        if (!good) n = 0;
+        return good;
+    }
+};
+
+// Work item `item` of a packed batch in which good sequence b, of n rows, has count(b, n) items (>= 0):
+// the sequence and the item's index inside it.  Every warp computes it for itself, 32 sequences at a time;
+// the result is the same in every thread.  False when there are fewer items.
 template <typename F>
-__device__ __forceinline__ bool find_item(int batch, int item, F count, int& b, int& j) {
+__device__ __forceinline__ bool find_item(const int32_t* __restrict__ cu, int batch, int rows, int item, F count, int& b, int& j) {
     const int lane = threadIdx.x & 31;
     int before = 0;
+    RowWalk walk;
     for (int base = 0; base < batch; base += 32) {
-        const int n = base + lane < batch ? count(base + lane) : 0;
+        int start, len;
+        walk.step(cu, batch, base, rows, start, len);
+        const int n = len > 0 ? count(base + lane, len) : 0;
         int x = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -53,15 +92,22 @@ __device__ __forceinline__ bool find_item(int batch, int item, F count, int& b, 
     return false;
 }
 
-// Records ENERGON_DEVICE_BAD_LENGTH if some sequence's rows lie outside [0, rows]; called by
-// one warp of one block of a launch.
-__device__ __forceinline__ void check_rows(const int32_t* __restrict__ cu, int batch, int rows, int32_t* status) {
+// Records ENERGON_DEVICE_BAD_LENGTH if some sequence is not good, or also(b, n) says so of one that is; called
+// by one warp of one block of a launch.
+template <typename F>
+__device__ __forceinline__ void check_rows(const int32_t* __restrict__ cu, int batch, int rows, int32_t* status, F also) {
     bool bad = false;
-    for (int b = threadIdx.x & 31; b < batch; b += 32) {
-        int s, n;
-        bad |= !seq_rows(cu, b, rows, s, n);
+    RowWalk walk;
+    for (int base = 0; base < batch; base += 32) {
+        int start, n;
+        const int b = base + (threadIdx.x & 31);
+        if (!walk.step(cu, batch, base, rows, start, n)) bad = true;
+        else if (b < batch) bad |= also(b, n);
     }
     if (bad) status_or(status, ENERGON_DEVICE_BAD_LENGTH);
+}
+__device__ __forceinline__ void check_rows(const int32_t* __restrict__ cu, int batch, int rows, int32_t* status) {
+    check_rows(cu, batch, rows, status, [](int, int) { return false; });
 }
 
 __device__ __forceinline__ float warp_max(float v) {

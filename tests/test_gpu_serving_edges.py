@@ -74,3 +74,85 @@ def test_cache_attention_scale_not_a_number(dt, n, which):
         assert torch.equal(o[:, :2], want[:, :2]) and torch.equal(lse[:, :2], wl[:, :2])
         assert bool(torch.isnan(o[:, 2:]).all()), p
         assert bool(torch.isnan(lse[:, 2:]).all()) if which == 2 else torch.equal(lse, wl), p
+
+# ------------------------------------------------------------------ offsets that step back
+
+
+def accepted(cu, rows):
+    """Which sequences are computed: rows inside [0, rows], and none between the first and the last row of those before."""
+    lo, hi, good = None, None, []
+    for a, b in zip(cu, cu[1:]):
+        inside = 0 <= a <= b <= rows
+        good.append(inside and (a == b or lo is None or a >= hi or b <= lo))
+        if inside and a < b:
+            lo, hi = (a, b) if lo is None else (min(lo, a), max(hi, b))
+    return good
+
+
+def stepping(seed, batch, rows):
+    """Offsets of `batch` sequences with some steps back and some outside the rows."""
+    r = np.random.default_rng(seed)
+    cu, at = [], int(r.integers(0, rows // 2))
+    for _ in range(batch + 1):
+        cu.append(at)
+        at += int(r.choice([0, 1, 40, 130, 300]))
+        kind = r.random()
+        if kind < 0.08:
+            at = int(r.integers(0, rows))
+        elif kind < 0.11:
+            at = int(r.choice([-5, rows + 9, 1 << 30]))
+        at = at if at < rows or kind >= 0.08 else rows
+        if at > rows and kind >= 0.11:
+            at = int(r.integers(0, rows // 2))
+    return cu
+
+
+STEPS = [([0, 1000, 10, 2000, 3000, 4000], 4000), ([5, 5, -1, 0, 10, 400, 399, 700], 700), ([600, 900, 0, 300, 600, 650], 900),
+         ([0, 128, 0, 128, 0, 128, 0, 128, 256], 256)] + [(stepping(s, n, 2500), 2500) for s, n in ((1, 20), (2, 70), (3, 200))]
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("case", range(len(STEPS)))
+def test_prompts_offsets_that_step_back(dt, case):
+    """Sequences whose rows belong to others too are left out; all the others are computed, none twice."""
+    cu, rows = STEPS[case]
+    H, kv, d, B = 2, 1, 64, len(cu) - 1
+    g = gen(case)
+    q, k, v = (randn(g, rows, h, d, dt=DT[dt]) for h in (H, kv, kv))
+    o, lse = torch.full((rows, H, d), 7.0, dtype=DT[dt], device="cuda"), torch.full((H, rows), 7.0, device="cuda")
+    w, want_w = (torch.full((kv, rows), 7.0, device="cuda") for _ in range(2))
+    want, want_l, good = o.clone(), lse.clone(), accepted(cu, rows)
+    code, st, st2 = capi.DTYPE_OF[DT[dt]], status(), status()
+    capi.energon_prompt_attention(q, H * d, k, kv * d, v, kv * d, ints(cu), B, rows, H, kv, d, code, 0.2, o, H * d, lse, st)
+    assert int(st) == (OK if all(good) else capi.ENERGON_DEVICE_BAD_LENGTH) and not all(good)
+    for a, b, ok in zip(cu, cu[1:], good):
+        if ok and a < b:
+            x, l = call_prompt(q[a:b], k[a:b], v[a:b], [b - a], 0.2)
+            want[a:b], want_l[:, a:b] = x, l
+            part = torch.empty(kv, b - a, device="cuda")
+            capi.energon_prompt_key_weights(q[a:b], H * d, k[a:b], kv * d, l.contiguous(), starts([b - a]), 1, b - a, H, kv, d,
+                                            code, 0.2, 33, part)
+            want_w[:, a:b] = part
+    assert torch.equal(o, want) and torch.equal(lse, want_l)
+    capi.energon_prompt_key_weights(q, H * d, k, kv * d, want_l, ints(cu), B, rows, H, kv, d, code, 0.2, 33, w, st2)
+    assert torch.equal(w, want_w) and int(st2) == capi.ENERGON_DEVICE_BAD_LENGTH
+
+
+@pytest.mark.parametrize("case", range(len(STEPS)))
+def test_append_offsets_that_step_back(case):
+    cu, rows = STEPS[case]
+    kv, d, P, B = 1, 64, 16, len(cu) - 1
+    good = accepted(cu, rows)
+    lens = [min(max(b - a, 0), rows) + 3 for a, b in zip(cu, cu[1:])]
+    pages = sum(-(-n // P) for n in lens)
+    t, x = make(pages, kv, P, d, seed=case), randn(gen(case), rows, kv, d)
+    table, h, st = tables(lens, P, pages, 2), host(make(pages, kv, P, d, seed=case)), status()
+    xs = f64(x).astype(np.float32)
+    for i, (a, b) in enumerate(zip(cu, cu[1:])):
+        if good[i]:
+            ref.append(h, table[i:i + 1], [lens[i]], xs[a:b], xs[a:b], None, [b - a])
+    c = capi.make_kv_cache(*t)
+    capi.energon_kv_append(c, ints(table), table.shape[1], ints(lens), x, kv * d, x.clone(), kv * d, None, ints(cu), B, rows,
+                           capi.ENERGON_F32, st)
+    assert int(st) == capi.ENERGON_DEVICE_BAD_LENGTH
+    same(t, h)
