@@ -105,7 +105,7 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         tmem_alloc(&tmem_slot, 2 * BQ);
         tmem_relinquish();
     }
-    if (lin == 0 && rank == 0 && warp == 0 && !__any_sync(0xffffffffu, stop)) check_rows(p.cu, p.batch, p.rows, p.status);
+    if (lin == 0 && rank == 0 && tid < 32 && !stopped(p.status)) check_rows(p.cu, p.batch, p.rows, p.status);
     int b, blk, start, n;
     auto count = [](int, int len) { return (len + BK - 1) / BK; };
     if (!find_item(p.cu, p.batch, p.rows, (int)(lin / p.n_kv), count, b, blk)) {

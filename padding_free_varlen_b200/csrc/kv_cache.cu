@@ -74,9 +74,6 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], uint64_t neg_scale
     return make_uint2(w[0], w[1]);
 }
 
-// Whether a sequence of `len` tokens can end with n new ones.
-__device__ __forceinline__ bool append_ok(const AppendArgs& a, int len, int n) { return len_ok(len, a.c) && n <= len; }
-
 constexpr int APPEND_THREADS = 256;
 constexpr int APPEND_HELD = 128 * 128 / 8 / APPEND_THREADS;  // pieces of 8 elements per thread of the largest page
 }  // namespace
@@ -88,17 +85,25 @@ __global__ void __launch_bounds__(APPEND_THREADS, sizeof(T) == 4 ? 2 : 4) kv_app
     const CacheArgs& c = a.c;
     if (block_stopped(c.status)) return;
     const int tid = threadIdx.x, P = c.page_len, d = c.head_dim, log_p = __ffs(P) - 1;
-    if (blockIdx.x == 0 && blockIdx.y == 0 && tid < 32)
-        check_rows(a.cu, c.batch, a.rows, c.status, [&](int i, int n) { return !append_ok(a, c.lens[i], n); });
+    const int32_t* const lens = c.lens;
+    const int64_t room = (int64_t)c.max_pages * P;
+    // A sequence of l tokens that ends with m new ones has to hold them and to fit in its pages.
+    auto fits = [room](int l, int m) { return m <= l && l <= room; };
+    if (blockIdx.x == 0 && blockIdx.y == 0 && tid < 32) {
+        bool bad = false;
+        int s, m;
+        for (int i = tid; i < c.batch; i += 32) bad |= !seq_rows(a.cu, i, a.rows, s, m) || !fits(lens[i], m);
+        if (bad) status_or(c.status, ENERGON_DEVICE_BAD_LENGTH);
+    }
     int b, j, start, n;
-    auto count = [&](int i, int m) {
-        const int l = c.lens[i];
-        return append_ok(a, l, m) ? ((l - 1) >> log_p) - ((l - m) >> log_p) + 1 : 0;
+    auto count = [lens, fits, log_p](int i, int m) {
+        const int l = lens[i];
+        return m > 0 && fits(l, m) ? ((l - 1) >> log_p) - ((l - m) >> log_p) + 1 : 0;
     };
     if (!find_item(a.cu, c.batch, a.rows, blockIdx.x, count, b, j)) return;
     seq_rows(a.cu, b, a.rows, start, n);
     // new tokens: rows start .. start + n - 1 at positions len - n .. len - 1
-    const int len = c.lens[b];
+    const int len = lens[b];
     const int at = ((len - n) >> log_p) + j;                               // page of the sequence
     const int s0 = max(len - n - at * P, 0), s1 = min(len - at * P, P);    // its slots that receive tokens
     const int row0 = start + at * P + s0 - (len - n);

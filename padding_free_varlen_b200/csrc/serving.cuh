@@ -29,23 +29,15 @@ __device__ __forceinline__ bool seq_rows(const int32_t* __restrict__ cu, int b, 
 // Passes over the sequences of a packed batch, 32 at a time (a lane each), and tells which are good: rows in
 // [0, rows], none of them between the first and the last row of the sequences before.  Good sequences then
 // share no row, so that none is written twice and the launches' bounds on the work hold whatever the
-// offsets are.  While all offsets ascend that costs one vote; behind the first sequence that is not good the rows
-// passed so far are followed by scans.
+// offsets are.  (Where all offsets ascend in [0, rows] all sequences are good.)
 struct RowWalk {
-    int lo = 0x7fffffff, hi = -1;  // first and last + 1 of the rows passed (where `straight` is false)
-    bool straight = true;
-    // Sequence base + lane: its rows; false where it is not good (n = 0 then), true behind the last one (n = 0).
-    __device__ __forceinline__ bool step(const int32_t* __restrict__ cu, int batch, int base, int rows, int& start, int& n) {
+    int lo = 0x7fffffff, hi = -1;  // first and last + 1 of the rows passed so far
+    // Sequence base + lane: its first row, and how many rows; n = 0 where it is not good, and behind the last one.
+    __device__ __forceinline__ void step(const int32_t* __restrict__ cu, int batch, int base, int rows, int& start, int& n) {
         constexpr unsigned ALL = 0xffffffffu;
         const int lane = threadIdx.x & 31;
         start = n = 0;
-        const bool inside = base + lane >= batch || seq_rows(cu, base + lane, rows, start, n);
-        if (straight) {
-            if (__all_sync(ALL, inside)) return true;
-            straight = false;
-            const int first = cu[0], now = cu[base];
-            if (first < now) lo = first, hi = now;
-        }
+        if (base + lane < batch) seq_rows(cu, base + lane, rows, start, n);
         int a = n > 0 ? start : 0x7fffffff, z = n > 0 ? start + n : -1;  // of this sequence and those before
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -56,58 +48,77 @@ struct RowWalk {
         int before_lo = __shfl_up_sync(ALL, a, 1), before_hi = __shfl_up_sync(ALL, z, 1);
         if (lane == 0) before_lo = lo, before_hi = hi;
         lo = __shfl_sync(ALL, a, 31), hi = __shfl_sync(ALL, z, 31);
-        const bool good = inside && (n == 0 || start >= before_hi || start + n <= before_lo);
-        if (!good) n = 0;
-        return good;
+        if (start < before_hi && start + n > before_lo) n = 0;
     }
 };
 
-// Work item `item` of a packed batch in which good sequence b, of n rows, has count(b, n) items (>= 0):
-// the sequence and the item's index inside it.  Every warp computes it for itself, 32 sequences at a time;
-// the result is the same in every thread.  False when there are fewer items.
-template <typename F>
-__device__ __forceinline__ bool find_item(const int32_t* __restrict__ cu, int batch, int rows, int item, F count, int& b, int& j) {
+// The item among 32 sequences, this lane's with n items, `before` items before them: the lane, or -1, and the
+// item's index inside its sequence.
+__device__ __forceinline__ int item_lane(int item, int n, int& before, int& j) {
     const int lane = threadIdx.x & 31;
-    int before = 0;
+    int x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, item < before + x);
+    if (past) {
+        const int l = __ffs(past) - 1;
+        j = item - before - __shfl_sync(0xffffffffu, x - n, l);
+        return l;
+    }
+    before += __shfl_sync(0xffffffffu, x, 31);
+    return -1;
+}
+// find_item where some sequence's rows are not in [0, rows]; -1 when there are fewer items.  (Apart: in line this
+// code, hardly ever run, cost the kernels around it 2 to 4 %.)
+template <typename F>
+__device__ __noinline__ int2 find_item_walk(const int32_t* __restrict__ cu, int batch, int rows, int item, F count) {
     RowWalk walk;
+    int before = 0, j = 0;
     for (int base = 0; base < batch; base += 32) {
         int start, len;
         walk.step(cu, batch, base, rows, start, len);
-        const int n = len > 0 ? count(base + lane, len) : 0;
-        int x = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
+        const int b = base + (threadIdx.x & 31);
+        const int l = item_lane(item, b < batch ? count(b, len) : 0, before, j);
+        if (l >= 0) return make_int2(base + l, j);
+    }
+    return make_int2(-1, 0);
+}
+// Work item `item` of a packed batch in which good sequence b, of n rows, has count(b, n) items (>= 0; none
+// of n = 0): the sequence and the item's index inside it.  Every warp computes it for itself, 32 sequences at
+// a time; the result is the same in every thread.  False when there are fewer items.
+template <typename F>
+__device__ __forceinline__ bool find_item(const int32_t* __restrict__ cu, int batch, int rows, int item, F count, int& b, int& j) {
+    int before = 0;
+    for (int base = 0; base < batch; base += 32) {
+        const int i = base + (threadIdx.x & 31);
+        int start, len = 0;
+        const bool inside = i >= batch || seq_rows(cu, i, rows, start, len);
+        const int l = item_lane(item, i < batch ? count(i, len) : 0, before, j);
+        if (__any_sync(0xffffffffu, !inside)) {
+            const int2 at = find_item_walk(cu, batch, rows, item, count);
+            b = at.x, j = at.y;
+            return b >= 0;
         }
-        const unsigned past = __ballot_sync(0xffffffffu, item < before + x);
-        if (past) {
-            const int l = __ffs(past) - 1;
+        if (l >= 0) {
             b = base + l;
-            j = item - before - __shfl_sync(0xffffffffu, x - n, l);
             return true;
         }
-        before += __shfl_sync(0xffffffffu, x, 31);
     }
     return false;
 }
 
-// Records ENERGON_DEVICE_BAD_LENGTH if some sequence is not good, or also(b, n) says so of one that is; called
-// by one warp of one block of a launch.
-template <typename F>
-__device__ __forceinline__ void check_rows(const int32_t* __restrict__ cu, int batch, int rows, int32_t* status, F also) {
+// Records ENERGON_DEVICE_BAD_LENGTH if some sequence is not good; called by one warp of one block of a
+// launch.  (Only a step back of the offsets, itself a sequence of less than 0 rows, makes sequences meet.)
+__device__ __forceinline__ void check_rows(const int32_t* __restrict__ cu, int batch, int rows, int32_t* status) {
     bool bad = false;
-    RowWalk walk;
-    for (int base = 0; base < batch; base += 32) {
-        int start, n;
-        const int b = base + (threadIdx.x & 31);
-        if (!walk.step(cu, batch, base, rows, start, n)) bad = true;
-        else if (b < batch) bad |= also(b, n);
+    for (int b = threadIdx.x & 31; b < batch; b += 32) {
+        int s, n;
+        bad |= !seq_rows(cu, b, rows, s, n);
     }
     if (bad) status_or(status, ENERGON_DEVICE_BAD_LENGTH);
-}
-__device__ __forceinline__ void check_rows(const int32_t* __restrict__ cu, int batch, int rows, int32_t* status) {
-    check_rows(cu, batch, rows, status, [](int, int) { return false; });
 }
 
 __device__ __forceinline__ float warp_max(float v) {
