@@ -489,8 +489,10 @@ ENERGON_API int energon_kv_append(const energon_kv_cache* cache, const int32_t* 
  *               (a common prefix); with accumulate the order in which they add to a shared
  *               page is not fixed.
  * The products run on the tensor cores with the codes as fp16 numbers (exact) and fp32 sums.
- * 16-bit queries enter as they are, fp32 queries to 22 bits; the probabilities, times their
- * page's value scale, are rounded to fp16 for the product with the value codes (fp32: to 22 bits).
+ * fp16 queries enter as they are, and bf16 queries but for bits below 2^-39 of the row's largest
+ * element; fp32 queries enter to 22 bits.  The probabilities, times their page's value scale, are rounded
+ * to fp16 for the product with the value codes (fp32: to 22 bits), none finer than 2^-30 of the
+ * largest such product of its query or than 2^-126 of the largest value scale.
  * An empty sequence gives o = 0 and lse = -infinity.  Tokens of a bad page count as masked.  A query
  * element that is not finite gives NaN in its head's o, lse and added weights.
  *   workspace   energon_cache_attention_workspace_bytes bytes, 256-byte aligned; its contents

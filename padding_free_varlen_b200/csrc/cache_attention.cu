@@ -9,8 +9,10 @@
 // 16-bit numbers).  A code is exact in fp16.  A query row is scaled by a power of two to
 // below 2^15: fp16 and bf16 queries are then exact (bf16 elements below 2^-28 of the row's largest
 // lose bits below 2^-39 of it), fp32 queries are held as two fp16 terms (2^-22 of the element).
-// The scales stay outside the sums over d: one factor per (page, head) for the scores, and for the
-// values p * scale / (largest scale met so far), times 2^7, as fp16 (two terms for fp32 outputs).
+// The scales stay outside the sums over d: one factor per (page, head) for the scores, and the values'
+// factor belongs to the probability: p * scale is rounded to fp16 (two terms for fp32 outputs) in a unit of the
+// query's own, a power of two that the largest product p * scale met so far reaches 2^5 to 2^15 of.  A unit
+// from the scales alone would round away tokens of small scales beside a page of a large scale without weight.
 //
 // A warp takes 32 tokens at a time: K and V rows land in its own ring of STAGES buffers by
 // TMA (the box of a page's tokens, swizzled so that the 16-byte reads of the fragments hit
@@ -44,7 +46,10 @@ constexpr int SUPER = 32;    // steps whose page entries a warp holds (one per l
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float GROW = 8.0f;      // log2 of the growth that a running maximum may lag behind
-constexpr float P_UP = 128.0f;    // 2^7: the exponentials, at most 2^GROW, fill the range of fp16
+// Probability times value scale is held in units of 2^(unit - P_UP): at most 2^(P_UP + GROW) of them, the range
+// of fp16.  A unit lies in [UNIT_MIN, UNIT_MAX] (it and its reciprocal are normal numbers) and at most 2^UNIT_SPAN
+// below the largest scale (scale / unit does not overflow).
+constexpr float P_UP = 7.0f, UNIT_MIN = -119.0f, UNIT_MAX = 133.0f, UNIT_SPAN = 112.0f;
 
 template <int HD>
 struct DCfg {
@@ -133,6 +138,10 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t w) {
 }
 // 2^k for -126 <= k <= 127.
 __device__ __forceinline__ float power_of_two(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
+// The same of a float that holds a whole number (the low bits of 1.5 * 2^23 + 127 + k are those of 127 + k).
+__device__ __forceinline__ float power_of_two(float k) { return __uint_as_float(__float_as_uint(12582912.0f + 127.0f + k) << 23); }
+// The smallest whole number l with |x| < 2^l (-126 below the normal range, 129 for infinity and NaN).
+__device__ __forceinline__ float log2_above(float x) { return (float)(int)(__float_as_uint(x) << 1 >> 24) - 126.0f; }
 __device__ __forceinline__ uint32_t pair_f16(float a, float b) { return pack2<__half>(a, b); }
 // What fp16 leaves of a pair.
 __device__ __forceinline__ uint32_t rest_f16(float a, float b, uint32_t hi) {
@@ -253,10 +262,11 @@ __global__ void __launch_bounds__(CW * 32, QT == 8 && sizeof(T) == 2 ? 3 : 2) ca
             }
     }
 
-    float m[R][2], l[R][2], acc[R][ND / 2][4];
+    // Exponentials refer to m and the outputs to m + unit (in log2); both are whole, so that rescaling is exact.
+    float m[R][2], l[R][2], unit[R][2], acc[R][ND / 2][4];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        m[r][0] = m[r][1] = -INFINITY, l[r][0] = l[r][1] = 0.0f;
+        m[r][0] = m[r][1] = -INFINITY, l[r][0] = l[r][1] = 0.0f, unit[r][0] = unit[r][1] = UNIT_MIN;
 #pragma unroll
         for (int i = 0; i < ND / 2; ++i)
 #pragma unroll
@@ -265,7 +275,7 @@ __global__ void __launch_bounds__(CW * 32, QT == 8 && sizeof(T) == 2 ? 3 : 2) ca
     // scores are kept as [token][query of the group]; this lane's place for its sequence's token g
     float* const scores = sp.ws.scores + (((int64_t)b * c.n_kv + kvh) * sp.ws.stride + g) * sp.ws.group + qt * QT + 2 * cc;
     const int log_p = __ffs(P) - 1;
-    float v_most = 0.0f;  // largest value scale met: the unit of acc
+    float lowest = UNIT_MIN;  // the least unit that the scales met so far allow
     bool ok = true;
     uint8_t* mine = ring + warp * C::WARP;
     const uint64_t policy = streaming();
@@ -301,18 +311,19 @@ __global__ void __launch_bounds__(CW * 32, QT == 8 && sizeof(T) == 2 ? 3 : 2) ca
                 }
             }
         }
-        const float v_new = fmaxf(v_most, warp_max(fmaxf(vs[0], vs[1])));
-        if (v_new > v_most && v_most > 0.0f) {
-            const float by = v_most / v_new;
+        const float v_top = warp_max(fmaxf(log2_above(vs[0]), log2_above(vs[1])));
+        if (v_top - UNIT_SPAN > lowest) {
+            lowest = v_top - UNIT_SPAN;
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
-                for (int i = 0; i < ND / 2; ++i)
+                for (int e = 0; e < 2; ++e) {
+                    const float by = exp2_fast(fminf(unit[r][e] - lowest, 0.0f));
+                    unit[r][e] = fmaxf(unit[r][e], lowest);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[r][i][e] *= by;
+                    for (int y = 0; y < ND / 2; ++y) acc[r][y][e] *= by, acc[r][y][2 + e] *= by;
+                }
         }
-        v_most = v_new;
-        if (v_most > 0.0f) vs[0] = vs[0] / v_most * P_UP, vs[1] = vs[1] / v_most * P_UP;  // (else 0, or NaN)
 
         auto fetch = [&](int i) {
             const int p0 = __shfl_sync(0xffffffffu, tile[0], i), p1 = __shfl_sync(0xffffffffu, tile[1], i);
@@ -386,7 +397,7 @@ __global__ void __launch_bounds__(CW * 32, QT == 8 && sizeof(T) == 2 ? 3 : 2) ca
             const float ks0 = __shfl_sync(0xffffffffu, ks[0], i), ks1 = __shfl_sync(0xffffffffu, ks[1], i);
             const float vs0 = __shfl_sync(0xffffffffu, vs[0], i), vs1 = __shfl_sync(0xffffffffu, vs[1], i);
             const bool whole = t0 + STEP <= t_end && p0 >= 0 && p1 >= 0;
-            bool grown = false;
+            bool grown = false;  // beyond what the maximum, or the unit, may lag behind
 #pragma unroll
             for (int r = 0; r < R; ++r) {
 #pragma unroll
@@ -408,7 +419,8 @@ __global__ void __launch_bounds__(CW * 32, QT == 8 && sizeof(T) == 2 ? 3 : 2) ca
             for (int r = 0; r < R; ++r) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    grown |= max3(fmaxf(x[0][r][e], x[0][r][2 + e]), x[1][r][e], x[1][r][2 + e]) - m[r][e] > GROW;
+                    grown |= max3(fmaxf(x[0][r][e], x[0][r][2 + e]), x[1][r][e], x[1][r][2 + e]) - m[r][e] >
+                             fminf(GROW, unit[r][e] + (GROW - v_top));
             }
             if (a.accumulate) {
                 float* to = scores + (int64_t)t0 * sp.ws.group;
@@ -430,19 +442,28 @@ __global__ void __launch_bounds__(CW * 32, QT == 8 && sizeof(T) == 2 ? 3 : 2) ca
                         }
             }
             if (__any_sync(0xffffffffu, grown)) {
+                const float v0 = log2_above(vs0), v1 = log2_above(vs1);
 #pragma unroll
                 for (int r = 0; r < R; ++r)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float mx = max3(fmaxf(x[0][r][e], x[0][r][2 + e]), x[1][r][e], x[1][r][2 + e]);
+                        const float x0 = fmaxf(x[0][r][e], x[0][r][2 + e]), x1 = fmaxf(x[1][r][e], x[1][r][2 + e]);
+                        float mx = fmaxf(x0, x1);
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                        if (mx - m[r][e] > GROW) {
-                            const float alpha = m[r][e] == -INFINITY ? 0.0f : exp2_fast(m[r][e] - mx);
-                            m[r][e] = mx;
-                            l[r][e] *= alpha;
+                        const bool up = mx - m[r][e] > GROW;
+                        const float top = up ? ceilf(mx) : m[r][e], ref = top == -INFINITY ? 0.0f : top;
+                        float most = fmaxf(x0 - ref + v0, x1 - ref + v1);  // log2 of probability times scale
 #pragma unroll
-                            for (int y = 0; y < ND / 2; ++y) acc[r][y][e] *= alpha, acc[r][y][2 + e] *= alpha;
+                        for (int o = 4; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+                        const float now = up ? unit[r][e] + (m[r][e] - top) : unit[r][e];  // the same unit, from the new maximum
+                        const float next = fminf(fmaxf(most - now > GROW ? ceilf(most) : now, lowest), UNIT_MAX);
+                        if (up || next != now) {
+                            const float by = exp2_fast(now - next);
+                            if (up) l[r][e] *= exp2_fast(m[r][e] - top);
+                            m[r][e] = top, unit[r][e] = next;
+#pragma unroll
+                            for (int y = 0; y < ND / 2; ++y) acc[r][y][e] *= by, acc[r][y][2 + e] *= by;
                         }
                     }
             }
@@ -453,13 +474,14 @@ __global__ void __launch_bounds__(CW * 32, QT == 8 && sizeof(T) == 2 ? 3 : 2) ca
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     const float ms0 = m[r][0] == -INFINITY ? 0.0f : m[r][0], ms1 = m[r][1] == -INFINITY ? 0.0f : m[r][1];
+                    const float f0 = vf * power_of_two(P_UP - unit[r][0]), f1 = vf * power_of_two(P_UP - unit[r][1]);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const float e0 = exp2_fast(x[u][r][2 * h] - ms0), e1 = exp2_fast(x[u][r][2 * h + 1] - ms1);
                         l[r][0] += e0, l[r][1] += e1;
-                        const uint32_t hi = pair_f16(e0 * vf, e1 * vf);
+                        const uint32_t hi = pair_f16(e0 * f0, e1 * f1);
                         pf[0][r][h] = transposed(hi);
-                        if constexpr (TERMS == 2) pf[1][r][h] = transposed(rest_f16(e0 * vf, e1 * vf, hi));
+                        if constexpr (TERMS == 2) pf[1][r][h] = transposed(rest_f16(e0 * f0, e1 * f1, hi));
                     }
                 }
                 uint32_t w[4][ND / 4];  // [tokens 2c, 2c + 1, 2c + 8, 2c + 9][this lane's d / 8 codes]
@@ -516,7 +538,7 @@ __global__ void __launch_bounds__(CW * 32, QT == 8 && sizeof(T) == 2 ? 3 : 2) ca
 #pragma unroll
             for (int w = 1; w < CW; ++w) top = fmaxf(top, sh_m[w][q]);
             const float mw = sh_m[warp][q];
-            const float f = mw == -INFINITY ? 0.0f : exp2_fast(mw - top) * (v_most * (1.0f / P_UP));
+            const float f = mw == -INFINITY ? 0.0f : exp2_fast(mw - top) * power_of_two(unit[r][e] - P_UP);
             float* to = out + (warp * QT + q) * LD + ND * g;
 #pragma unroll
             for (int y = 0; y < ND / 4; ++y)

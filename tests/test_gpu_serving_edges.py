@@ -156,3 +156,43 @@ def test_append_offsets_that_step_back(case):
                            capi.ENERGON_F32, st)
     assert int(st) == capi.ENERGON_DEVICE_BAD_LENGTH
     same(t, h)
+
+# ------------------------------------------------------------------ value scales far apart
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("P", [16, 64])
+@pytest.mark.parametrize("small", [1e-3, 1e-6, 1e-10, 1e-30])
+@pytest.mark.parametrize("big", ["first", "last", "between", "every other"])
+@pytest.mark.parametrize("pages", [40, 400])
+def test_cache_attention_large_scale_without_weight(dt, P, small, big, pages):
+    """Pages of value scale 1 whose tokens have next to no probability beside pages of small scales that have
+    all of it: the error is relative to what the output is made of."""
+    H, kv, d, n = 6, 2, 64, pages * P - 5
+    t, g = make(pages, kv, P, d, seed=P), gen(P)
+    t[0][:] = torch.randint(1, 4, t[0].shape, device="cuda", generator=g, dtype=torch.int8)
+    t[2][:], t[3][:] = 0.01, small
+    at = {"first": [0], "last": [pages - 1], "between": [pages // 2, pages // 2 + 3], "every other": list(range(0, pages, 2))}[big]
+    for p in at:                                           # 60 and more below the others' scores, in units of log2 87
+        t[0][p], t[2][p], t[3][p] = -100, 0.01, 1.0
+    if small == 1e-3:
+        t[2][at] = 0.0025                                  # 15 below: their part of the output counts a little
+    q = torch.ones(1, H, d, device="cuda", dtype=DT[dt]) + randn(g, 1, H, d, dt=DT[dt]) / 16
+    table = np.arange(pages, dtype=np.int32)[None]
+    o, lse = call_decode(t, table, [n], q, 1.0)
+    ro, rlse, probs, mag, smag = ref.decode(host(t), table, [n], f64(q), 1.0)
+    # (the pages without weight have larger scores, whose errors do not count: less than 2^-28 of the output)
+    smag = ref.decode(host(t), table, [n], f64(q), 1.0, good=lambda b, i: i // P not in at)[4]
+    ds, u = score_error(d, smag) * (4 if dt == "f32" else 1), half_step(DT[dt])
+    scale = np.repeat(t[3].cpu().numpy().astype(np.float64), P, 0)[:n]        # [n, kv]
+    top = np.array([[(probs[0, h] * scale[:, h // 3]).max() for h in range(H)]])
+    # a probability times its scale: half a step of fp16 (2^-22 in two terms), but not finer than 2^-25 of a unit
+    # that the largest of them reaches 2^5 of
+    rel = 2 * ds[..., None] + n * 2.0 ** -24 + 2.0 ** -19 + (u if dt != "f32" else 0.0) + (2.0 ** -11 if dt != "f32" else 2.0 ** -22)
+    tol = mag * rel + u * np.abs(ro) + n * 2.0 ** -30 * 127 * top[..., None]
+    if dt == "f16":
+        tol = tol + 2.0 ** -25
+    err = np.abs(f64(o) - ro)
+    assert (err <= tol).all(), float((err / tol).max())
+    lerr = np.abs(f64(lse) - rlse)
+    assert (lerr <= ds + n * 2.0 ** -24 + 2.0 ** -21 * (1 + np.abs(rlse))).all()
