@@ -10,8 +10,8 @@
 //              read from TMEM (over the columns of S)
 //   softmax    four warps, a thread per query: row of S to registers, maximum, exponentials, P rounded to
 //              16 bits back to TMEM.  O is rescaled only when the maximum grew by more than 2^8:
-//              until then the exponentials are at most 2^8, in range of both types, and the common
-//              factor leaves with the sum.
+//              until then the exponentials are at most 2^8 (fp16: times 2^7), in range of both types, and
+//              the common factor leaves with the sum.
 //   scan       two warps: rows of V behind the sequence and values that are not finite are
 //              zeroed in the blocks that cross the diagonal (there 0 * NaN would reach earlier
 //              rows); the latter are noted and added to the rows that see them at the end.
@@ -43,6 +43,10 @@ constexpr int QBOX = BM * 128;          // bytes of 128 rows x 64 columns of 16 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float GROW = 8.0f;            // log2 of the growth that the running maximum may lag behind
+// log2 of the factor of fp16 probabilities: with GROW they fill its range, and those down to 2^-21 of the
+// largest keep all their bits (without it many small ones together could vanish).  It leaves with the sum.
+template <typename T>
+constexpr float P_UP = std::is_same<T, __half>::value ? 7.0f : 0.0f;
 
 constexpr int BN = 64;                  // keys per block
 
@@ -489,7 +493,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             read_item(k, it, true);
             if (it.n == 0) break;
             const int q0 = it.q0(), s = q0 + tid, nb = it.blocks(), scan0 = it.scan0();
-            float m = -INFINITY, mc = 0.0f;  // the maximum that the exponentials refer to, and times c (0 for -infinity)
+            float m = -INFINITY, mc = 0.0f;  // the maximum that the exponentials refer to, and times c less P_UP (0 for -infinity)
             uint64_t sum[4] = {0, 0, 0, 0};  // pairs of partial sums (+0.0)
             for (int kb = 0; kb < nb; ++kb, ++g) {
                 const uint32_t S = S0 + (g & 1) * BN;
@@ -510,7 +514,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 const float mx = max_of<BN>(x);
                 if (kb == 0) {
                     m = mx;
-                    mc = m == -INFINITY ? 0.0f : m * a.c;
+                    mc = m == -INFINITY ? 0.0f : m * a.c - P_UP<T>;
                 } else if (__any_sync(0xffffffffu, (mx - m) * a.c > GROW)) {
                     // O is at rest once the products of block kb - 1 are done; those of kb - 2 were before S,
                     // those of kb wait for this thread: the phase is the barrier's current or last one
@@ -519,8 +523,9 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     tc_fence_after();
                     float by = 1.0f;
                     if ((mx - m) * a.c > GROW) {
-                        by = m == -INFINITY ? 0.0f : exp2_fast(mc - mx * a.c);
-                        m = mx, mc = mx * a.c;
+                        const float now = mx * a.c - P_UP<T>;
+                        by = m == -INFINITY ? 0.0f : exp2_fast(mc - now);
+                        m = mx, mc = now;
                     }
 #pragma unroll
                     for (int y = 0; y < 4; ++y) sum[y] = mul2(sum[y], two(by, by));

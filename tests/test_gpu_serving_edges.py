@@ -196,3 +196,32 @@ def test_cache_attention_large_scale_without_weight(dt, P, small, big, pages):
     assert (err <= tol).all(), float((err / tol).max())
     lerr = np.abs(f64(lse) - rlse)
     assert (lerr <= ds + n * 2.0 ** -24 + 2.0 ** -21 * (1 + np.abs(rlse))).all()
+
+# ------------------------------------------------------------------ probabilities below the normal range of fp16
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("below", [14.5, 20.5, 23.4375, 27.0])
+def test_prompt_many_small_probabilities(dt, d, below):
+    """One key takes nearly all the weight and its value is 0; the others, `below` powers of two less each,
+    make the output: it is as exact as their own rounding."""
+    H, kv, lens = 2, 1, [900, 70]
+    T, g = sum(lens), gen(d)
+    q, k = torch.zeros(T, H, d, device="cuda", dtype=DT[dt]), torch.zeros(T, kv, d, device="cuda", dtype=DT[dt])
+    q[:, :, 0] = 1
+    v = (torch.rand(T, kv, d, device="cuda", generator=g) + 1).to(DT[dt]) * 2 ** 10
+    for first in (0, 900):
+        k[first, 0, 0], v[first] = below, 0
+    scale = float(np.log(2.0))
+    o, lse = call_prompt(q, k, v, lens, scale)
+    ro, rlse, mag, smag = ref.prompt(f64(q), f64(k), f64(v), lens, scale)
+    ds, u = score_error(d, smag), half_step(DT[dt])
+    tol = mag * (2 * ds.T[..., None] + 900 * 2.0 ** -24 + 2.0 ** -20 + u) + u * np.abs(ro)
+    if dt == "f16":
+        # 2^-25 of a unit in which a probability of 1 is 2^7; the output's own smallest half step
+        tol = tol + 900 * 2.0 ** -32 * 2.0 ** 11 + 2.0 ** -25
+    err = np.abs(f64(o) - ro)
+    assert (err <= tol).all(), float((err / tol).max())
+    lerr = np.abs(f64(lse) - rlse)
+    assert (lerr <= ds + 900 * 2.0 ** -24 + 2.0 ** -22 * (1 + np.abs(rlse))).all()
