@@ -26,8 +26,9 @@
  *    the ABI; energon_last_error() gives a message for the calling thread.
  *  - Device status word (int32_t, caller-owned, device memory): invalid lengths
  *    and bounded-wait timeouts are detected on the device and recorded there
- *    (ENERGON_DEVICE_* bits).  Kernels of a call that find a nonzero word do no
- *    work.  Read it after synchronising the stream.
+ *    (ENERGON_DEVICE_* bits).  Kernels of a call that find ENERGON_DEVICE_BAD_LENGTH or
+ *    ENERGON_DEVICE_TIMEOUT in it do no work (the serving calls: see there).  Read
+ *    it after synchronising the stream.
  */
 #ifndef ENERGON_RCE_H
 #define ENERGON_RCE_H
@@ -212,7 +213,9 @@ ENERGON_API size_t energon_workspace_bytes(const energon_layer_config* cfg, int 
  *   T = cu_seqlens[batch] rows are read / written.  y_packed == x_packed allowed.
  *   max_len: the largest sequence length (pad_len); sizes the launch grids.
  *   d_status: optional device status word (NULL allowed); kernels skip work when
- *   it is nonzero and OR ENERGON_DEVICE_TIMEOUT into it if a bounded wait expires.
+ *   it holds ENERGON_DEVICE_BAD_LENGTH or ENERGON_DEVICE_TIMEOUT (not for what
+ *   energon_kv_append and its kind say of a page or a value), and OR
+ *   ENERGON_DEVICE_TIMEOUT into it if a bounded wait expires.
  * LayerNorm statistics, accumulation and softmax are fp32.  The first LayerNorm
  * is folded into the QKV GEMM (its operand is the layer input times ln1_g, one
  * rounding, exact when ln1_g is 1; the epilogue applies the row statistics), Q
@@ -387,7 +390,9 @@ ENERGON_API int energon_sched_fifo(const energon_request* reqs, int n, int max_b
  * are.  Row pointers are 16-byte aligned and row distances a multiple of 16 bytes
  * (else ENERGON_ERR_MISALIGNED).  `scale` multiplies q . k; it is finite and > 0.
  * d_status is optional; bits are OR-ed into it.  What is wrong with one sequence does not
- * stop the others: the kernels do no work only where they find ENERGON_DEVICE_TIMEOUT.
+ * stop the others: the kernels do no work only where they find ENERGON_DEVICE_TIMEOUT.  A word
+ * that layers share stops those at ENERGON_DEVICE_BAD_LENGTH too: give them words of their own,
+ * or clear the word, where layers should go on behind a sequence that was left out.
  * Buffers written by a call do not overlap what it reads unless stated.
  * All sums, softmax statistics and weights are fp32.  Two calls that use different
  * outputs and workspaces may run at once.  Results do not depend on timing: no sum's

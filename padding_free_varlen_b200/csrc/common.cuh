@@ -76,8 +76,11 @@ __device__ __forceinline__ float gelu_tanh_fast(float v) {
 
 // ----------------------------------------------------------------- status word
 
+// What stops the layers: offsets that are not to be trusted, and a wait that ran out.  The other bits tell of
+// single values and pages of the key/value cache and may stand in a word that the layers share.
 __device__ __forceinline__ bool status_bad(const int32_t* st) {
-    return st != nullptr && *reinterpret_cast<const volatile int32_t*>(st) != 0;
+    return st != nullptr &&
+           (*reinterpret_cast<const volatile int32_t*>(st) & (ENERGON_DEVICE_BAD_LENGTH | ENERGON_DEVICE_TIMEOUT)) != 0;
 }
 __device__ __forceinline__ void status_or(int32_t* st, int32_t bits) {
     if (st) atomicOr(st, bits);

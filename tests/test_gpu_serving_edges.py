@@ -225,3 +225,40 @@ def test_prompt_many_small_probabilities(dt, d, below):
     assert (err <= tol).all(), float((err / tol).max())
     lerr = np.abs(f64(lse) - rlse)
     assert (lerr <= ds + 900 * 2.0 ** -24 + 2.0 ** -22 * (1 + np.abs(rlse))).all()
+
+# ------------------------------------------------------------------ one status word for all calls
+
+
+@pytest.mark.parametrize("dtype", [synth.F32, synth.F16])
+def test_a_notice_of_the_cache_does_not_stop_the_layers(dtype):
+    """A layer and the cache's calls share a status word: what an append says about a value or a page leaves
+    the layer's work alone; a wait that ran out and a bad length still stop it."""
+    shape = synth.LayerShape(256, 4, 1024)
+    lens, S = [5, 9], 16
+    T, tdt = sum(lens), TORCH_OF_SYNTH[dtype]
+    _, dev_w = gpu_layer_weights(shape, 0, 7, dtype, synth.WeightRecipe(w_std=0.02, bias_std=0.1, gamma_std=0.2, beta_std=0.1))
+    cfg = capi.make_config(shape.hidden, shape.n_heads, shape.ffn, SYNTH_TO_ENERGON[dtype])
+    n = capi.energon_workspace_bytes(cfg, len(lens), S)
+    ws, w = torch.empty(n, dtype=torch.uint8, device="cuda"), capi.make_weights(dev_w)
+    x = randn(gen(1), len(lens) * S, shape.hidden, dt=tdt)
+
+    def layer(st):
+        y = torch.full_like(x, 7.0)
+        capi.energon_layer_forward(cfg, w, x, starts(lens), len(lens), S, y, st, ws, n)
+        return y
+    st = status()
+    want = layer(st)
+    assert int(st) == OK and not bool((want[:T] == 7).all(1).any())
+    # the layer's keys and values go to a cache, one of them infinite
+    t = make(2, 4, 16, 64)
+    kv = want[:T].view(T, 4, 64).clone()
+    kv[3, 1, 5] = float("inf")
+    call_append(t, np.array([[0], [1]], np.int32), lens, kv, kv.clone(), lens, st=st)
+    assert int(st) == capi.ENERGON_DEVICE_NONFINITE
+    assert torch.equal(layer(st)[:T], want[:T]) and int(st) == capi.ENERGON_DEVICE_NONFINITE
+    call_append(t, np.array([[0], [9]], np.int32), lens, kv, kv.clone(), lens, st=st)
+    assert int(st) == capi.ENERGON_DEVICE_NONFINITE | capi.ENERGON_DEVICE_BAD_PAGE
+    assert torch.equal(layer(st)[:T], want[:T])
+    for bit in (capi.ENERGON_DEVICE_BAD_LENGTH, capi.ENERGON_DEVICE_TIMEOUT):
+        st = status() + bit
+        assert bool((layer(st) == 7).all()) and int(st) == bit
