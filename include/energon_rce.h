@@ -487,7 +487,8 @@ ENERGON_API int energon_kv_append(const energon_kv_cache* cache, const int32_t* 
  * Attention of one new token per sequence over its cached tokens:
  *     o_j = sum_{t < cache_lens[b]} softmax_t(scale q_j . K(t)) V(t)
  *   q, o        [batch] rows of n_heads heads, dtype fp32, fp16 or bf16
- *   max_len     no cache_lens entry is larger (sizes the launch and the workspace)
+ *   max_len     no cache_lens entry is larger (sizes the launch and the workspace); at most
+ *               0x7c000000
  *   lse         optional [batch, n_heads] fp32: log sum_t exp(scale q . K(t))
  *   accumulate  nonzero: adds each token's probabilities, summed over the query heads of
  *               its kv head, to cache->weight (required then).  Sequences may share pages
@@ -518,7 +519,8 @@ ENERGON_API int energon_cache_attention(const energon_kv_cache* cache, const int
  * of the pages named by new_page_table [batch, new_max_pages]; weights move with them.  Each
  * kv head keeps its own tokens, all keep the same number.
  *   new_lens    out [batch] int32: min(cache_lens[b], budget); may be cache_lens
- *   budget      >= 1, at most new_max_pages * page_len;  0 <= recent <= budget
+ *   budget      >= 1, at most new_max_pages * page_len and 0x7c000000;  0 <= recent <= budget
+ *   max_len     as in energon_cache_attention
  * A new page's scale is the largest scale among the old pages its tokens come from; a code
  * is multiplied by the fp32 quotient old scale / new scale and rounded to the nearest
  * integer, ties to even (tokens of the page with the largest scale keep their codes).  Slots

@@ -749,6 +749,9 @@ int energon_kv_append(const energon_kv_cache* cache, const int32_t* page_table, 
     });
 }
 
+// Bound on max_len and budget: the kernels' positions may run one step (at most 2^25 tokens) ahead in 32 bits.
+static constexpr int MOST_TOKENS = 0x7c000000;
+
 size_t energon_cache_attention_workspace_bytes(const energon_kv_cache* cache, int batch, int max_len, int n_heads,
                                                int accumulate) {
     if (!cache || batch < 0 || max_len < 0 || n_heads < 1 || cache->n_kv_heads < 1) return 0;
@@ -763,7 +766,7 @@ int energon_cache_attention(const energon_kv_cache* cache, const int32_t* page_t
         const char* what = "cache attention";
         if (int r = check_cache(what, cache, page_table, max_pages, cache_lens, batch)) return r;
         if (int r = check_heads(what, n_heads, cache->n_kv_heads, cache->head_dim, dtype, scale)) return r;
-        if (max_len < 0 || max_len > 0x7fffff00) return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: bad max_len %d", what, max_len);
+        if (max_len < 0 || max_len > MOST_TOKENS) return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: bad max_len %d", what, max_len);
         const int64_t width = (int64_t)n_heads * cache->head_dim;
         if (int r = check_rows_arg(what, "q", q, batch, ld_q, width, dtype)) return r;
         if (int r = check_rows_arg(what, "o", o, batch, ld_o, width, dtype)) return r;
@@ -796,10 +799,10 @@ int energon_cache_evict(const energon_kv_cache* cache, const int32_t* page_table
         const char* what = "cache evict";
         if (int r = check_cache(what, cache, page_table, max_pages, cache_lens, batch)) return r;
         if (!cache->weight || (batch > 0 && (!new_page_table || !new_lens))) return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: NULL pointer", what);
-        if (max_len < 0 || max_len > 0x7fffff00) return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: bad max_len %d", what, max_len);
-        if (budget < 1 || recent < 0 || recent > budget)
-            return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: budget %d and recent %d (budget >= 1, 0 <= recent <= budget)", what,
-                        budget, recent);
+        if (max_len < 0 || max_len > MOST_TOKENS) return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: bad max_len %d", what, max_len);
+        if (budget < 1 || budget > MOST_TOKENS || recent < 0 || recent > budget)
+            return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: budget %d and recent %d (1 <= budget <= %d, 0 <= recent <= budget)",
+                        what, budget, recent, MOST_TOKENS);
         if (new_max_pages < 1 || (int64_t)new_max_pages * cache->page_len < budget)
             return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: %d new pages do not hold a budget of %d", what, new_max_pages, budget);
         if (int r = check_ws(what, workspace, ws_bytes, energon_cache_evict_workspace_bytes(cache, batch, budget))) return r;
