@@ -7,7 +7,7 @@
 #include <stdio.h>
 #include <string.h>
 
-#include <string>
+#include <exception>
 #include <vector>
 
 #include "../../include/energon_rce.h"
@@ -17,16 +17,19 @@ using namespace energon;
 
 namespace {
 
-thread_local std::string g_last_error;
+// Text of the last error; it takes no memory, so that it can say that there is none.
+struct Message {
+    char text[512];
+    void clear() { text[0] = 0; }
+};
+thread_local Message g_last_error;
 uint64_t g_timeout_ns = 2000000000ull;
 
 int fail(int code, const char* fmt, ...) {
-    char buf[512];
     va_list ap;
     va_start(ap, fmt);
-    vsnprintf(buf, sizeof(buf), fmt, ap);
+    vsnprintf(g_last_error.text, sizeof(g_last_error.text), fmt, ap);
     va_end(ap);
-    g_last_error = buf;
     return code;
 }
 
@@ -322,13 +325,13 @@ namespace energon {
 // Lets the other translation units of the library report through energon_last_error().
 void record_error(int code, const char* msg) {
     if (code == ENERGON_OK) g_last_error.clear();
-    else g_last_error = msg;
+    else fail(code, "%s", msg);
 }
 }  // namespace energon
 
 extern "C" {
 
-const char* energon_last_error(void) { return g_last_error.c_str(); }
+const char* energon_last_error(void) { return g_last_error.text; }
 
 void energon_set_wait_timeout_us(uint32_t timeout_us) {
     g_timeout_ns = (uint64_t)(timeout_us == 0 ? 1 : timeout_us) * 1000ull;
@@ -611,8 +614,10 @@ int guarded(const char* what, F&& f) {
     try {
         g_last_error.clear();
         return f();
+    } catch (const std::exception& e) {
+        return fail(ENERGON_ERR_CUDA, "%s: %s", what, e.what());
     } catch (...) {
-        return ENERGON_ERR_CUDA;
+        return fail(ENERGON_ERR_CUDA, "%s: an exception", what);
     }
 }
 
