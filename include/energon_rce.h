@@ -277,7 +277,8 @@ ENERGON_API int energon_selftest_bounded_wait(int32_t* d_status, uint32_t timeou
 ENERGON_API int energon_kernel_binary_version(int* version);
 
 /* Upper limit, in microseconds, of every bounded wait inside the kernels
- * (default 2,000,000).  Process-wide. */
+ * (default 2,000,000; it may be passed by some 15 microseconds).  What is in flight when
+ * a wait runs out is granted at least a second more to arrive.  Process-wide. */
 ENERGON_API void energon_set_wait_timeout_us(uint32_t timeout_us);
 
 /*

@@ -123,6 +123,10 @@ __device__ __forceinline__ uint64_t global_ns() {
     return t;
 }
 
+// After how many tries (a power of two, less one) a wait looks at its limit: reading the clock takes longer
+// than a try, but 32 tries take some 15 us, too long for a limit below a millisecond.
+__device__ __forceinline__ uint32_t tries_between_looks(uint64_t timeout_ns) { return timeout_ns < 1000000ull ? 0u : 31u; }
+
 // Bounded wait for the phase of `parity` to complete.  Gives up (returns false)
 // after `timeout_ns` of wall time, after 2^30 polls, or - when `abort_flag` is
 // non-null - as soon as another role of the block has set it.
@@ -130,9 +134,10 @@ static __device__ __noinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t pa
                                                uint64_t timeout_ns) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = global_ns();
+    const uint32_t tries = tries_between_looks(timeout_ns);
     for (uint32_t it = 1; it < (1u << 30); ++it) {
         if (mbar_try_wait(bar, parity)) return true;
-        if ((it & 31u) == 0) {
+        if ((it & tries) == 0) {
             if (abort_flag != nullptr && *abort_flag) return false;
             if (global_ns() - t0 > timeout_ns) return false;
         }

@@ -138,9 +138,10 @@ __device__ __forceinline__ bool wait_in_line(uint64_t* bar, uint32_t parity, con
                                              uint64_t timeout_ns) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = global_ns();
+    const uint32_t tries = tries_between_looks(timeout_ns);
     for (uint32_t it = 1; it < (1u << 30); ++it) {
         if (mbar_try_wait(bar, parity)) return true;
-        if ((it & 31u) == 0 && (*abort_flag || global_ns() - t0 > timeout_ns)) return false;
+        if ((it & tries) == 0 && (*abort_flag || global_ns() - t0 > timeout_ns)) return false;
     }
     return false;
 }

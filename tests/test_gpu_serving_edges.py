@@ -262,3 +262,86 @@ def test_a_notice_of_the_cache_does_not_stop_the_layers(dtype):
     for bit in (capi.ENERGON_DEVICE_BAD_LENGTH, capi.ENERGON_DEVICE_TIMEOUT):
         st = status() + bit
         assert bool((layer(st) == 7).all()) and int(st) == bit
+
+# ------------------------------------------------------------------ waits that run out
+
+
+@pytest.fixture
+def short_waits():
+    capi.energon_set_wait_timeout_us(1)
+    yield
+    capi.energon_set_wait_timeout_us(2000000)
+
+
+def busy(stream, n=6):
+    """Memory traffic beside the call, so that its loads take longer than the limit."""
+    a = torch.empty(1 << 28, dtype=torch.int32, device="cuda")
+    with torch.cuda.stream(stream):
+        for _ in range(n):
+            a.copy_(a.roll(1))
+
+
+def test_waits_that_run_out(short_waits):
+    """A limit of a microsecond: a call ends and
+    says that a wait ran out, or has computed everything; a call with its limit back, on the same buffers, has the
+    usual bits.  What ran out stops the calls behind it."""
+    g, side, ran_out = gen(1), torch.cuda.Stream(), 0
+    P, lens, ctx = 64, [1500, 700, 130, 64] * 4, [9000, 3000, 500, 70]
+    for dt, H, kv, d in ((torch.bfloat16, 16, 4, 128), (torch.float16, 8, 8, 64), (torch.float16, 24, 2, 128)):
+        T, code, scale = sum(lens), capi.DTYPE_OF[dt], d ** -0.5
+        q, k, v = (randn(g, T, h, d, dt=dt) for h in (H, kv, kv))
+        cu, B = starts(lens), len(lens)
+        t = make(220, kv, P, d, seed=2)
+        table, one = tables(ctx, P, 220, 3), randn(g, len(ctx), H, d, dt=dt)
+        cache, tab, ctx_lens = capi.make_kv_cache(*t), ints(table), ints(ctx)
+        ws = torch.empty(capi.energon_cache_attention_workspace_bytes(cache, len(ctx), max(ctx), H, 1), dtype=torch.uint8, device="cuda")
+        held = t[4].clone()
+
+        def prompt(out, st):
+            capi.energon_prompt_attention(q, H * d, k, kv * d, v, kv * d, cu, B, T, H, kv, d, code, scale, out[0], H * d, out[1], st)
+
+        def weights(window):
+            def call(out, st):
+                capi.energon_prompt_key_weights(q, H * d, k, kv * d, lse, cu, B, T, H, kv, d, code, scale, window, out[0], st)
+            return call
+
+        def decode(out, st):
+            t[4].copy_(held)
+            capi.energon_cache_attention(cache, tab, table.shape[1], ctx_lens, len(ctx), max(ctx), one, H * d, H, code, scale, out[0],
+                                         H * d, out[1], 1, st, ws, ws.numel())
+            out[2].copy_(t[4])
+        new = lambda *s, dt=torch.float32: torch.full(s, 7.0, dtype=dt, device="cuda")  # noqa: E731
+        shapes = {prompt: lambda: [new(T, H, d, dt=dt), new(H, T)], weights(40): lambda: [new(kv, T)],
+                  weights(1 << 30): lambda: [new(kv, T)],
+                  decode: lambda: [new(len(ctx), H, d, dt=dt), new(len(ctx), H), torch.empty_like(held)]}
+        capi.energon_set_wait_timeout_us(2000000)
+        want = prompt_out = shapes[prompt]()
+        prompt(want, status())
+        lse = prompt_out[1]
+        for call, outs in shapes.items():
+            capi.energon_set_wait_timeout_us(2000000)
+            want, st = outs(), status()
+            call(want, st)
+            assert int(st) == OK
+            for i in range(6):
+                capi.energon_set_wait_timeout_us(1)
+                out, st = outs(), status()
+                torch.cuda.synchronize()
+                if i % 2:
+                    busy(side)
+                call(out, st)
+                torch.cuda.synchronize()
+                assert int(st) in (OK, capi.ENERGON_DEVICE_TIMEOUT)
+                if int(st) == OK:
+                    assert all(torch.equal(x, y) for x, y in zip(out, want))
+                else:
+                    ran_out += 1
+                    behind = outs()
+                    capi.energon_set_wait_timeout_us(2000000)
+                    call(behind, st)
+                    assert all(bool((x == 7).all()) for x in behind[:2])
+                capi.energon_set_wait_timeout_us(2000000)
+                again, st = outs(), status()
+                call(again, st)
+                assert int(st) == OK and all(torch.equal(x, y) for x, y in zip(again, want))
+    assert ran_out
