@@ -256,7 +256,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     // TMEM is read, and work is issued, by whole warps: their lanes give up together
     auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
     PromptItem it;
-    // Item k of this block; false where a wait ran out.  `leave`: this warp needs it no more.
+    // Item k of this block, which is there.  `leave`: this warp needs it no more.
     auto read_item = [&](int k, PromptItem& to, bool leave) {
         const int at = k % ITEMS;
         const volatile int4& v = items[at];
@@ -269,7 +269,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 
     if (warp == SOFT) {
         // ---- loader: announces the items, loads Q, then K(0), K(1), V(0), K(2), V(1), ... of each
-        int x = blockIdx.x, y = blockIdx.y, k = 0, nk = 0, nv = 0, asked = 0;
+        int x = blockIdx.x, y = blockIdx.y, k = 0, nq = 0, nk = 0, nv = 0, asked = 0;  // n.: loads issued
         uint32_t ins = 0;  // bit i: parity of v_in[i]'s next use
         bool ok = dead == 0, more = true;
         if (lane == 0) tma_prefetch_desc(&tm_q), tma_prefetch_desc(&tm_k), tma_prefetch_desc(&tm_v);
@@ -303,6 +303,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     for (int h = 0; h < HD / 64; ++h)
                         tma_load_2d(base + h * QBOX, &tm_q, &q_full, it.head * HD + 64 * h, it.start + it.q0());
                 }
+                if (ok) ++nq;
                 for (int ik = 0, iv = 0; ok && iv < nb;) {
                     const bool keys = ik < nb && ik - iv < 2;
                     const int kb = keys ? ik : iv, g = keys ? nk : nv, at = g % C::RING;
@@ -337,7 +338,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
         if (ok) announce(make_int4(0, 0, 0, 0));
         // All copies have landed before the block ends, also where a wait ran out.
-        if (k > 0) mbar_wait_bounded(&q_full, (k - 1) & 1, nullptr, landing_limit(p.timeout_ns));
+        if (nq > 0) mbar_wait_bounded(&q_full, (nq - 1) & 1, nullptr, landing_limit(p.timeout_ns));
         for (int g = max(0, nk - C::RING); g < nk; ++g) mbar_wait_bounded(&k_full[g % C::RING], (g / C::RING) & 1, nullptr, landing_limit(p.timeout_ns));
         for (int g = max(0, nv - C::RING); g < nv; ++g) mbar_wait_bounded(&v_full[g % C::RING], (g / C::RING) & 1, nullptr, landing_limit(p.timeout_ns));
         for (int i = 0; i < C::RING; ++i)  // (an unused one passes: the phase before its first counts as done)

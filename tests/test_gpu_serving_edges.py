@@ -282,8 +282,8 @@ def busy(stream, n=6):
 
 
 def test_waits_that_run_out(short_waits):
-    """A limit of a microsecond: a call ends and
-    says that a wait ran out, or has computed everything; a call with its limit back, on the same buffers, has the
+    """A limit of a microsecond: a call ends, in far less than the second that it grants copies in flight, and
+    says that a wait ran out or has computed everything; a call with its limit back, on the same buffers, has the
     usual bits.  What ran out stops the calls behind it."""
     g, side, ran_out = gen(1), torch.cuda.Stream(), 0
     P, lens, ctx = 64, [1500, 700, 130, 64] * 4, [9000, 3000, 500, 70]
@@ -326,11 +326,15 @@ def test_waits_that_run_out(short_waits):
             for i in range(6):
                 capi.energon_set_wait_timeout_us(1)
                 out, st = outs(), status()
+                a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
                 torch.cuda.synchronize()
                 if i % 2:
                     busy(side)
+                a.record()
                 call(out, st)
+                b.record()
                 torch.cuda.synchronize()
+                assert a.elapsed_time(b) < 500.0
                 assert int(st) in (OK, capi.ENERGON_DEVICE_TIMEOUT)
                 if int(st) == OK:
                     assert all(torch.equal(x, y) for x, y in zip(out, want))
