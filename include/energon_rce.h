@@ -277,8 +277,8 @@ ENERGON_API int energon_selftest_bounded_wait(int32_t* d_status, uint32_t timeou
 ENERGON_API int energon_kernel_binary_version(int* version);
 
 /* Upper limit, in microseconds, of every bounded wait inside the kernels
- * (default 2,000,000; it may be passed by some 15 microseconds).  What is in flight when
- * a wait runs out is granted at least a second more to arrive.  Process-wide. */
+ * (default 2,000,000; it may be passed by some 15 microseconds).  What a serving call has in
+ * flight when a wait runs out is granted at least a second more to arrive.  Process-wide. */
 ENERGON_API void energon_set_wait_timeout_us(uint32_t timeout_us);
 
 /*
@@ -391,7 +391,8 @@ ENERGON_API int energon_sched_fifo(const energon_request* reqs, int n, int max_b
  * are.  Row pointers are 16-byte aligned and row distances a multiple of 16 bytes
  * (else ENERGON_ERR_MISALIGNED).  `scale` multiplies q . k; it is finite and > 0.
  * d_status is optional; bits are OR-ed into it.  What is wrong with one sequence does not
- * stop the others: the kernels do no work only where they find ENERGON_DEVICE_TIMEOUT.  A word
+ * stop the others: the kernels do no work only where they find ENERGON_DEVICE_TIMEOUT (where a
+ * wait ran out, the outputs of that call and a cache that it writes are not to be used).  A word
  * that layers share stops those at ENERGON_DEVICE_BAD_LENGTH too: give them words of their own,
  * or clear the word, where layers should go on behind a sequence that was left out.
  * Buffers written by a call do not overlap what it reads unless stated.
@@ -493,8 +494,8 @@ ENERGON_API int energon_kv_append(const energon_kv_cache* cache, const int32_t* 
  *   lse         optional [batch, n_heads] fp32: log sum_t exp(scale q . K(t))
  *   accumulate  nonzero: adds each token's probabilities, summed over the query heads of
  *               its kv head, to cache->weight (required then).  Sequences may share pages
- *               (a common prefix); with accumulate the order in which they add to a shared
- *               page is not fixed.
+ *               (a common prefix), and a row of the table may name a page twice; with
+ *               accumulate the order of the additions to such a page is not fixed.
  * The products run on the tensor cores with the codes as fp16 numbers (exact) and fp32 sums.
  * fp16 queries enter as they are, and bf16 queries but for bits below 2^-39 of the row's largest
  * element; fp32 queries enter to 22 bits.  The probabilities, times their page's value scale, are rounded

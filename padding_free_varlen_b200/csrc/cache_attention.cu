@@ -23,8 +23,8 @@
 //
 // 64 sequences of 1 to 8192 tokens (261 thousand in all), 64 heads of 128, 8 kv heads, bf16: 104 us without
 // weights, 5.2 TB/s (0.79 of the measured copy rate), 134 us with them.  What bounds it: turning
-// a step's 8 KB of codes into fp16 takes 350 of the about 640 instructions of a step and warp (3 warps per
-// scheduler, 0.56 instructions a cycle); the scores cost 17 us to write and 20 us in the
+// a step's 8 KB of codes into fp16 takes 350 of the about 650 instructions of a step and warp (3 warps per
+// scheduler, 0.58 instructions a cycle); the scores cost 17 us to write and 20 us in the
 // second kernel, although they stay in L2.  Tried: four blocks per SM with
 // one buffer for V (143 us), splits of 512, 1024 and 4096 tokens (159, 140, 152 us) instead of 2048, queries
 // as the rows of the first product (half of a tile empty, 156 us).
@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(FIN) cache_finish_kernel(const FinishArgs fa) 
                     for (int k = 0; k < K; ++k)
                         if (t + k * FIN < end) sum[k] += exp2_fast(x[(int64_t)(t + k * FIN) * group + h] - lse2[h]);
             }
-            // a page of one sequence has one writer per call; sequences that share a page add in any order
+            // a page named once has one writer per call; sequences that share a page add in any order
 #pragma unroll
             for (int k = 0; k < K; ++k)
                 if ((unsigned)page[k] < (unsigned)c.n_pages)

@@ -233,7 +233,7 @@ cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t st) {
     const int64_t most = (int64_t)a.rows / a.c.page_len + 2 * (int64_t)some;
     const int64_t pages = most < a.rows ? most : a.rows;
     // A block finds its page by a chain of loads; where pages are many it takes several heads of it (about two
-    // rounds of blocks on the SMs).  16 prompts, 16 thousand tokens in all: 35 us, of which memory would
+    // rounds of blocks on the SMs).  16 prompts, 15 thousand tokens in all: 35 us, of which memory would
     // take 15; 48 single tokens: 7 us, a block for each page and head.
     int64_t parts = (4 * 148 * 2 + pages - 1) / pages;
     if (parts > 2 * a.c.n_kv) parts = 2 * a.c.n_kv;

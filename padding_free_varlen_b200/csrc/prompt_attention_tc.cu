@@ -4,7 +4,8 @@
 //   o_j(s) = sum_{t <= s} exp(c q_j(s) . k(t) - lse_j(s)) v(t)
 //
 // An item is a tile of 128 queries of one (sequence, head).  Its keys and values pass by once in blocks
-// of 64, with a running maximum and sum:
+// of 64, with a running maximum and sum (M. Milakov, N. Gimelshein, Online normalizer calculation for softmax,
+// 2018):
 //   loader     one warp: announces the items, loads Q tiles and K and V blocks by TMA
 //   products   one warp: S = Q K^T into TMEM (two buffers, up to two blocks ahead), O += P V with P
 //              read from TMEM (over the columns of S)
@@ -21,7 +22,7 @@
 // On 64 requests of 1 to 256 tokens that took 172 us where a block per item took 277.
 //
 // One prompt of 8192 tokens, 32 heads of 128, 8 kv heads, bf16: 455 us, 1210 TFLOP/s, 0.88 of the
-// sustained rate of a library matrix product here.  A step of 64 keys needs 620
+// sustained rate of a library matrix product here.  A step of 64 keys needs 640
 // cycles of the tensor cores (384 for the scores, which read both operands from shared memory, 256 for the
 // products with V) and 512 of the special function units (64 x 128 exponentials at 16 a cycle); taking a quarter of
 // the exponentials on the FMA pipe measured slower.  Tried and slower: 128 keys per block with one buffer of

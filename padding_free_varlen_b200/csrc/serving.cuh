@@ -201,8 +201,8 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 
 // 2^x of a pair without the special function unit (16 results per cycle and SM, where the FMA pipe
-// makes 128 operations): x = j + f with j whole and |f| <= 1/2, 2^f by a polynomial of degree 5 with
-// constant term 1 fitted for the smallest relative error (1.7e-7), times 2^j from j's bits.
+// makes 128 operations): x = j + f with j whole and |f| <= 1/2 (the reduction of W. J. Cody, W. Waite, Software
+// Manual for the Elementary Functions, 1980), 2^f by a polynomial of degree 5 with constant term 1 fitted for the smallest relative error (1.7e-7), times 2^j from j's bits.
 // x <= 126; below -126 the result is 0 or next to it; NaN stays NaN.
 __device__ __forceinline__ float2 exp2_poly(float2 x) {
     constexpr float MAGIC = 12582912.0f;  // 1.5 * 2^23: adding it rounds to a whole number
