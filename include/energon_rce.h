@@ -389,7 +389,7 @@ ENERGON_API int energon_sched_fifo(const energon_request* reqs, int n, int max_b
  * heads, [row][head][head_dim]; ld_* is the distance between rows in elements (at
  * least heads * head_dim), so that parts of a fused Q | K | V row can be passed as they
  * are.  Row pointers are 16-byte aligned and row distances a multiple of 16 bytes
- * (else ENERGON_ERR_MISALIGNED).  `scale` multiplies q . k; it is finite and > 0.
+ * (else ENERGON_ERR_MISALIGNED).  `scale` multiplies q . k; it is > 0 and at most 2e38.
  * d_status is optional; bits are OR-ed into it.  What is wrong with one sequence does not
  * stop the others: the kernels do no work only where they find ENERGON_DEVICE_TIMEOUT (where a
  * wait ran out, the outputs of that call and a cache that it writes are not to be used).  A word
@@ -478,7 +478,7 @@ typedef struct {
  * counts for the scale, and ENERGON_DEVICE_NONFINITE is set.
  * Otherwise slots that receive no token keep their codes.  A sequence with more new tokens
  * than its length sets ENERGON_DEVICE_BAD_LENGTH and is skipped, and so is one whose rows
- * energon_prompt_attention would skip.  A page must belong to one sequence.
+ * energon_prompt_attention would skip.  A page must belong to one sequence, and stand in its row once.
  */
 ENERGON_API int energon_kv_append(const energon_kv_cache* cache, const int32_t* page_table, int max_pages,
                                   const int32_t* cache_lens, const void* k, int64_t ld_k, const void* v, int64_t ld_v,
@@ -530,7 +530,7 @@ ENERGON_API int energon_cache_attention(const energon_kv_cache* cache, const int
  * A sequence of at most `budget` tokens is copied.  The new pages are other pages than the
  * old ones, or row b of new_page_table begins with the same pages as row b of page_table:
  * then the sequence is cut in place (nothing is done where nothing is cut).  Old pages are
- * otherwise left as they were.  A page must belong to one sequence.
+ * otherwise left as they were.  A page must belong to one sequence, and stand in its rows once.
  * Sequences with a bad length or page are left alone and get new_lens 0.
  *   workspace   energon_cache_evict_workspace_bytes bytes, 256-byte aligned; as above
  */

@@ -628,8 +628,9 @@ int check_heads(const char* what, int n_heads, int n_kv, int head_dim, int dtype
     if (n_heads > 32767) return fail(ENERGON_ERR_UNSUPPORTED, "%s: more than 32767 heads", what);
     if (head_dim != 64 && head_dim != 128)
         return fail(ENERGON_ERR_UNSUPPORTED, "%s: head_dim %d (supported: 64, 128)", what, head_dim);
-    if (!(scale > 0.0f) || scale > 3.0e38f)
-        return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: scale must be finite and > 0", what);
+    // (the kernels work with scale * log2(e), which has to be finite too)
+    if (!(scale > 0.0f) || scale > 2.0e38f)
+        return fail(ENERGON_ERR_INVALID_ARGUMENT, "%s: scale must be > 0 and at most 2e38", what);
     return ENERGON_OK;
 }
 

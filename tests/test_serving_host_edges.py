@@ -35,6 +35,13 @@ def test_cache_attention_refuses_lengths_at_the_end_of_32_bits(max_len):
             0, 0, 0, 1 << 24, 1 << 20)
 
 
+def test_scales_beyond_what_the_kernels_can_hold_are_refused():
+    for scale in (2.4e38, 2.9e38):
+        refused(INVALID, capi.energon_prompt_attention, Q, 512, Q, 512, Q, 512, Q, 2, 8, 4, 4, 128, capi.ENERGON_F16, scale, O, 512)
+        refused(INVALID, capi.energon_cache_attention, cache(), 4096, 4, 8192, 2, 64, Q, 256, 4, capi.ENERGON_F16, scale, O, 256, 0, 0, 0,
+                1 << 24, 1 << 20)
+
+
 OUT_OF_MEMORY = r"""
 #include <cstdio>
 #include <cstdlib>
