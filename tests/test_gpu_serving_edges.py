@@ -276,6 +276,7 @@ def short_waits():
 def busy(stream, n=6):
     """Memory traffic beside the call, so that its loads take longer than the limit."""
     a = torch.empty(1 << 28, dtype=torch.int32, device="cuda")
+    a.record_stream(stream)
     with torch.cuda.stream(stream):
         for _ in range(n):
             a.copy_(a.roll(1))
